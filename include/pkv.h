@@ -167,7 +167,8 @@ typedef struct pkv_plan_info {
     int32_t kind;
     int32_t num_work_items;    /* CTAs of the main kernel */
     int32_t num_partials;      /* split-KV partial states (0: no merge pass) */
-    int32_t mask_mode;         /* 0 none, 1 causal, 2 causal + window, 3 window only */
+    int32_t mask_mode;         /* 0 none, 1 causal, 2 causal + window, 3 window only,
+                                  4 causal + window + sinks, 5 window + sinks */
     int64_t workspace_bytes;   /* device memory owned by the plan */
     int64_t total_q;           /* query rows */
     int32_t kernels_per_run;   /* launches issued by one pkv_run */
@@ -216,6 +217,26 @@ typedef struct pkv_plan_caps {
  */
 PKV_API int pkv_plan_create_capturable(pkv_plan **out, const pkv_plan_desc *desc, const pkv_plan_caps *caps,
                                        void *stream);
+
+/*
+ * pkv_plan_create_sinks: a plan (capturable when `caps` is not NULL) whose first
+ * `num_sinks` keys stay visible under the window, as the attention sinks of models that
+ * run on with a bounded cache: key j is visible to the query at position p iff
+ *     (!causal || j <= p) && (window_left < 0 || j >= p - window_left || j < num_sinks).
+ * With no window, or num_sinks = 0, the plan is that of pkv_plan_create /
+ * pkv_plan_create_capturable. Every kind, head_dim, page size and kv_dtype is supported,
+ * and pkv_run, pkv_plan_update (which keeps num_sinks) and the other calls take the plan
+ * as any other. Pages of a request that hold neither one of its first num_sinks keys nor
+ * a key at or after p - window_left of one of its queries are not read, so their entries
+ * in kv_indices may be anything (pages given back to a pool, say); a decode split over
+ * several CTAs counts its splits over the visible keys.
+ * As for plans without sinks, the V rows of a prefill's pages that hold a visible key
+ * must be finite where the cache holds a key (an invisible one is weighed with 0).
+ * Returns as pkv_plan_create; PKV_ERR_INVALID_ARG also for num_sinks < 0,
+ * PKV_ERR_UNSUPPORTED for num_sinks > 2^24.
+ */
+PKV_API int pkv_plan_create_sinks(pkv_plan **out, const pkv_plan_desc *desc, int32_t num_sinks,
+                                  const pkv_plan_caps *caps, void *stream);
 
 /*
  * pkv_plan_update: re-plan a capturable plan for a new batch, in place: host arrays

@@ -67,6 +67,11 @@ def _load():
                 i64, p, p, p, p, p, i64, i64, i64, i64, i64, i64, ctypes.c_int,
                 ctypes.c_double, ctypes.c_double, ctypes.c_double, ctypes.c_double, p, ctypes.c_int,
                 p, p, p, i64, p, p]
+            lib.pkv_oracle_attention_sinks.restype = ctypes.c_int
+            lib.pkv_oracle_attention_sinks.argtypes = [
+                i64, p, p, p, p, p, i64, i64, i64, i64, i64, i64, ctypes.c_int, i64,
+                ctypes.c_double, ctypes.c_double, ctypes.c_double, ctypes.c_double, p, ctypes.c_int,
+                p, p, p, i64, p, p]
             lib.pkv_oracle_decode_fp8.restype = ctypes.c_int
             lib.pkv_oracle_decode_fp8.argtypes = [ctypes.c_int, p, i64, p]
             lib.pkv_oracle_set_threads.restype = ctypes.c_int
@@ -134,13 +139,14 @@ def set_threads(n: int = 0) -> int:
 def attention(*, qo_indptr, kv_indptr, kv_indices, kv_last_page_len, num_qo_heads,
               num_kv_heads, head_dim, page_size, window_left, causal, sm_scale, q, k_cache,
               v_cache, q_start=None, rows=None, num_pages=None, logits_soft_cap=0.0, k_scale=1.0,
-              v_scale=1.0):
+              v_scale=1.0, num_sinks=0):
     """Reference attention in float64.
 
     q: bf16 [total_q, H_qo, d]; k_cache, v_cache: [num_pages, P, H_kv, d] CPU torch
     tensors of bf16, float8_e4m3fn or float8_e5m2 (both the same), or uint16 arrays of
     bf16 bits. Returns (out, lse) as float64 arrays [n, H_qo, d] and [n, H_qo],
-    n = total_q, or len(rows) for a row subset.
+    n = total_q, or len(rows) for a row subset. num_sinks: the first keys that stay
+    visible under the window.
     """
     lib = _load()
     qo_indptr = _i32(qo_indptr)
@@ -166,10 +172,10 @@ def attention(*, qo_indptr, kv_indptr, kv_indices, kv_last_page_len, num_qo_head
         n = total_q
     out = np.zeros((n, num_qo_heads, head_dim), dtype=np.float64)
     lse = np.zeros((n, num_qo_heads), dtype=np.float64)
-    rc = lib.pkv_oracle_attention_kv(
+    rc = lib.pkv_oracle_attention_sinks(
         batch, _ptr(qo_indptr), _ptr(kv_indptr), _ptr(kv_indices), _ptr(kv_last_page_len),
         _ptr(q_start), num_qo_heads, num_kv_heads, head_dim, page_size, int(num_pages),
-        int(window_left), int(bool(causal)), float(sm_scale), float(logits_soft_cap), float(k_scale),
+        int(window_left), int(bool(causal)), int(num_sinks), float(sm_scale), float(logits_soft_cap), float(k_scale),
         float(v_scale), _ptr(qb), kv_dtype, _ptr(kb), _ptr(vb),
         _ptr(sel), 0 if sel is None else len(sel), _ptr(out), _ptr(lse))
     if rc != OK:

@@ -155,11 +155,12 @@ static int64_t request_kv_len(const int32_t *kv_indptr, const int32_t *kv_last_p
     return (n_pages - 1) * page_size + (int64_t)kv_last_page_len[b];
 }
 
-static int key_is_visible(int64_t j, int64_t p, int64_t window_left, int causal)
+/* The first num_sinks keys stay visible under the window (never beyond the causal limit). */
+static int key_is_visible(int64_t j, int64_t p, int64_t window_left, int causal, int64_t num_sinks)
 {
     if (causal && j > p)
         return 0;
-    if (window_left >= 0 && j < p - window_left)
+    if (window_left >= 0 && j < p - window_left && j >= num_sinks)
         return 0;
     return 1;
 }
@@ -195,14 +196,14 @@ static double logit_of(double dot, double scale, double cap)
     return cap > 0.0 ? cap * tanh(s / cap) : s;
 }
 
-int pkv_oracle_attention_kv(int64_t batch, const int32_t *qo_indptr, const int32_t *kv_indptr,
-                            const int32_t *kv_indices, const int32_t *kv_last_page_len,
-                            const int32_t *q_start, int64_t num_qo_heads, int64_t num_kv_heads,
-                            int64_t head_dim, int64_t page_size, int64_t num_pages,
-                            int64_t window_left, int causal, double sm_scale, double soft_cap,
-                            double k_scale, double v_scale, const uint16_t *q, int kv_dtype,
-                            const void *k_cache, const void *v_cache, const int64_t *rows,
-                            int64_t n_rows, double *out, double *lse)
+int pkv_oracle_attention_sinks(int64_t batch, const int32_t *qo_indptr, const int32_t *kv_indptr,
+                               const int32_t *kv_indices, const int32_t *kv_last_page_len,
+                               const int32_t *q_start, int64_t num_qo_heads, int64_t num_kv_heads,
+                               int64_t head_dim, int64_t page_size, int64_t num_pages,
+                               int64_t window_left, int causal, int64_t num_sinks, double sm_scale,
+                               double soft_cap, double k_scale, double v_scale, const uint16_t *q,
+                               int kv_dtype, const void *k_cache, const void *v_cache,
+                               const int64_t *rows, int64_t n_rows, double *out, double *lse)
 {
     const double scale = sm_scale * k_scale;
     if (batch < 0 || num_kv_heads <= 0 || num_qo_heads <= 0 || head_dim <= 0 || page_size <= 0)
@@ -244,7 +245,7 @@ int pkv_oracle_attention_kv(int64_t batch, const int32_t *qo_indptr, const int32
         int64_t n_visible = 0;
         int bad = 0;
         for (int64_t j = 0; j < kv_len; ++j) {
-            if (!key_is_visible(j, p, window_left, causal))
+            if (!key_is_visible(j, p, window_left, causal, num_sinks))
                 continue;
             int64_t page = kv_indices[(int64_t)kv_indptr[b] + j / page_size];
             if (page < 0 || page >= num_pages) {
@@ -271,7 +272,7 @@ int pkv_oracle_attention_kv(int64_t batch, const int32_t *qo_indptr, const int32
         /* Pass 2: sum of exp(s - m) and the weighted sum of V. */
         double denom = 0.0;
         for (int64_t j = 0; j < kv_len; ++j) {
-            if (!key_is_visible(j, p, window_left, causal))
+            if (!key_is_visible(j, p, window_left, causal, num_sinks))
                 continue;
             int64_t page = kv_indices[(int64_t)kv_indptr[b] + j / page_size];
             int64_t slot = (page * page_size + j % page_size) * num_kv_heads + hk;
@@ -291,6 +292,21 @@ int pkv_oracle_attention_kv(int64_t batch, const int32_t *qo_indptr, const int32
             lse[k_out * num_qo_heads + h] = m + log(denom);
     }
     return status;
+}
+
+int pkv_oracle_attention_kv(int64_t batch, const int32_t *qo_indptr, const int32_t *kv_indptr,
+                            const int32_t *kv_indices, const int32_t *kv_last_page_len,
+                            const int32_t *q_start, int64_t num_qo_heads, int64_t num_kv_heads,
+                            int64_t head_dim, int64_t page_size, int64_t num_pages,
+                            int64_t window_left, int causal, double sm_scale, double soft_cap,
+                            double k_scale, double v_scale, const uint16_t *q, int kv_dtype,
+                            const void *k_cache, const void *v_cache, const int64_t *rows,
+                            int64_t n_rows, double *out, double *lse)
+{
+    return pkv_oracle_attention_sinks(batch, qo_indptr, kv_indptr, kv_indices, kv_last_page_len, q_start,
+                                      num_qo_heads, num_kv_heads, head_dim, page_size, num_pages, window_left,
+                                      causal, 0, sm_scale, soft_cap, k_scale, v_scale, q, kv_dtype, k_cache,
+                                      v_cache, rows, n_rows, out, lse);
 }
 
 int pkv_oracle_attention_ext(int64_t batch, const int32_t *qo_indptr, const int32_t *kv_indptr,

@@ -23,7 +23,8 @@ LIB = os.path.join(PKG, "libpkv.so")
 
 SOURCES = ["pkv_api.cpp", "pkv_decode.cu", "pkv_decode_fp8.cu", "pkv_merge.cu", "pkv_prefill.cu",
            "pkv_prefill_fp8.cu",
-           "pkv_noalloc.cu", "pkv_indices.cu"]
+           "pkv_noalloc.cu", "pkv_indices.cu", "pkv_decode_sinks.cu", "pkv_prefill_sinks.cu",
+           "pkv_prefill_sinks_fp8.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -42,7 +43,8 @@ def _flags(extra_verbose=False):
 # Kernels that redistribute registers between warpgroups with setmaxnreg: the
 # launch allocation (threads x registers per thread) must be exactly what the
 # split assumes, or setmaxnreg.inc would wait for registers that never come.
-REGISTER_SPLIT = {"pkv_prefill.cu": ("prefill_pp_kernel", 168), "pkv_prefill_fp8.cu": ("prefill_pp_kernel", 168)}
+REGISTER_SPLIT = {src: ("prefill_pp_kernel", 168) for src in
+                  ("pkv_prefill.cu", "pkv_prefill_fp8.cu", "pkv_prefill_sinks.cu", "pkv_prefill_sinks_fp8.cu")}
 
 
 def _check_register_split(logs):

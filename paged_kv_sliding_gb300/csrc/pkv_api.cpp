@@ -69,6 +69,7 @@ struct pkv_plan {
     int staging_next = 0;
     int32_t *d_live = nullptr;  // live work items (capturable decode launches exit above it)
     int64_t total_kv = 0;       // ragged prefill: rows of the contiguous K/V
+    int sinks = 0;              // keys [0, sinks) stay visible under the window (0: none)
     int decode_tile = 64;  // decode: KV tokens per stage of the kernel
     int64_t total_q = 0;
     const int32_t *kv_indices = nullptr;  // borrowed device pointer
@@ -183,6 +184,55 @@ void visible_interval(int64_t p_min, int64_t p_max, int64_t kv_len, int window_l
     hi = causal ? std::min<int64_t>(kv_len - 1, p_max) : kv_len - 1;
 }
 
+// Clip `sinks` to the keys before the visible interval [lo, hi] of the positions up to
+// p_max. When they touch it, or it is empty, one range is left: [lo, hi] then holds it
+// and 0 is returned.
+int64_t separate_sinks(int64_t sinks, int64_t p_max, int64_t kv_len, bool causal, int64_t &lo, int64_t &hi)
+{
+    int64_t s = std::min(sinks, kv_len);
+    if (causal)
+        s = std::min(s, p_max + 1);
+    if (s <= 0)
+        return 0;
+    if (hi < lo) {  // the sinks alone
+        lo = 0;
+        hi = s - 1;
+        return 0;
+    }
+    if (s >= lo) {
+        lo = 0;
+        return 0;
+    }
+    return s;
+}
+
+// A split of a decode request: keys [0, sink_end) and [j0, j1).
+struct DecodePiece {
+    int64_t sink_end, j0, j1;
+};
+
+// Pieces of `per` visible keys each of the keys [0, s) and [lo, lo + n): the key ranges of
+// one request's splits. A piece across the gap keeps both ranges if it starts at key 0
+// and is cut there otherwise.
+std::vector<DecodePiece> cut_pieces(int64_t s, int64_t lo, int64_t n, int64_t per)
+{
+    std::vector<DecodePiece> out;
+    for (int64_t v0 = 0; v0 < s + n; v0 += per) {
+        const int64_t v1 = std::min(s + n, v0 + per);
+        if (v1 <= s) {
+            out.push_back({0, v0, v1});
+        } else if (v0 >= s) {
+            out.push_back({0, lo + v0 - s, lo + v1 - s});
+        } else if (v0 == 0) {
+            out.push_back({s, lo, lo + v1 - s});
+        } else {
+            out.push_back({0, v0, s});
+            out.push_back({0, lo, lo + v1 - s});
+        }
+    }
+    return out;
+}
+
 // Greedy longest-first assignment of item costs to `slots` equal workers; returns
 // the finishing time of the busiest worker.
 double simulate_makespan(std::vector<double> costs, int slots)
@@ -290,13 +340,17 @@ struct Schedule {
     int64_t total_q = 0;
 };
 
+// Largest num_sinks: packed rows and the keys they stand for then stay below 2^31.
+constexpr int kMaxSinks = 1 << 24;
+
 // Splits per request that a capturable decode plan's workspace holds.
 constexpr int kCapturableMaxSplits = 4;
 
 // capturable: one prefill list per SM and at most kCapturableMaxSplits decode splits
 // per request; fixed_tile > 0: the decode tile to use (a captured launch's variant).
+// sinks: keys [0, sinks) stay visible under the window (0: none).
 void build_schedule(const pkv_plan_desc &d, const std::vector<HostRequest> &reqs, int device, bool capturable,
-                    int fixed_tile, Schedule &sc)
+                    int fixed_tile, int sinks, Schedule &sc)
 {
     const int B = d.batch_size;
     const int group = d.num_qo_heads / d.num_kv_heads;
@@ -320,6 +374,8 @@ void build_schedule(const pkv_plan_desc &d, const std::vector<HostRequest> &reqs
     int num_counters = 0;
     int mask_mode = causal ? (W >= 0 ? kMaskCausalWindow : kMaskCausal)
                            : (W >= 0 ? kMaskWindow : kMaskNone);
+    if (sinks > 0)
+        mask_mode = causal ? kMaskCausalWindowSinks : kMaskWindowSinks;
 
     if (d.kind != PKV_DECODE) {
         const int T = prefill_kv_tile(d.head_dim);
@@ -330,18 +386,33 @@ void build_schedule(const pkv_plan_desc &d, const std::vector<HostRequest> &reqs
         const int64_t kv_align = d.kind == PKV_PREFILL_RAGGED || d.kv_dtype != PKV_BF16 ? 1
                                  : prefill_pp_tma_page_size(d.page_size, d.head_dim)    ? std::min(d.page_size, T)
                                                                                         : 1;
+        // Rows the window's tiles may follow the sinks at: a ragged box is a whole tile.
+        const int64_t join_align = d.kind == PKV_PREFILL_RAGGED ? T : kv_align;
         for (int b = 0; b < B; ++b) {
             const HostRequest &r = reqs[b];
             for (int64_t t0 = 0; t0 < r.qo_len; t0 += tq) {
                 int64_t nt = std::min<int64_t>(tq, r.qo_len - t0);
                 int64_t lo, hi;
-                visible_interval(r.q_start + t0, r.q_start + t0 + nt - 1, r.kv_len, W, causal, lo, hi);
+                const int64_t p_max = r.q_start + t0 + nt - 1;
+                visible_interval(r.q_start + t0, p_max, r.kv_len, W, causal, lo, hi);
+                const bool no_window = hi < lo;
+                const int64_t s = sinks > 0 ? separate_sinks(sinks, p_max, r.kv_len, causal, lo, hi) : 0;
                 // The item's KV tiles start at its first visible key, rounded down
                 // only as far as the loader needs (a page for TMA page boxes), not
                 // to a multiple of the tile: the window then spans the fewest tiles.
-                int32_t start = 0, ntl = 0;
-                if (hi >= lo) {
-                    start = (int32_t)(lo / kv_align * kv_align);
+                // Sinks come before it in packed rows, the window's following at `join`
+                // (sinks alone: no row from there on is a key of the request).
+                int32_t start = 0, ntl = 0, join = 0;
+                if (hi >= lo && no_window) {
+                    join = (int32_t)round_up(hi + 1, join_align);
+                    start = INT32_MAX / 2 + 1;
+                    ntl = (int32_t)(hi / T + 1);
+                } else if (hi >= lo) {
+                    const int64_t base = lo / kv_align * kv_align;
+                    if (round_up(s, join_align) < base) {
+                        join = (int32_t)round_up(s, join_align);
+                        start = (int32_t)(base - join);
+                    }
                     ntl = (int32_t)((hi - start) / T + 1);
                 }
                 // Start tile: the query block's index times the golden ratio,
@@ -350,7 +421,7 @@ void build_schedule(const pkv_plan_desc &d, const std::vector<HostRequest> &reqs
                 const double frac = std::fmod((double)(t0 / tq) * 0.6180339887498949, 1.0);
                 const int32_t rot = ntl > 1 ? std::min<int32_t>(ntl - 1, (int32_t)(frac * ntl)) : 0;
                 for (int hk = 0; hk < d.num_kv_heads; ++hk)
-                    p_items.push_back({b, hk, (int32_t)t0, (int32_t)nt, start, ntl, rot, 0});
+                    p_items.push_back({b, hk, (int32_t)t0, (int32_t)nt, start, ntl, rot, join});
             }
         }
         // Persistent CTAs, one per SM: longest-processing-time-first assignment of
@@ -389,13 +460,14 @@ void build_schedule(const pkv_plan_desc &d, const std::vector<HostRequest> &reqs
         }
     } else {
         const int head_blocks = (group + kDecodeRows - 1) / kDecodeRows;
-        std::vector<int64_t> lens(B), los(B);
+        std::vector<int64_t> lens(B), los(B), sink_lens(B);
         for (int b = 0; b < B; ++b) {
             int64_t lo, hi;
             const HostRequest &r = reqs[b];
             visible_interval(r.q_start, r.q_start, r.kv_len, W, causal, lo, hi);
+            sink_lens[b] = sinks > 0 ? separate_sinks(sinks, r.q_start, r.kv_len, causal, lo, hi) : 0;
             los[b] = lo;
-            lens[b] = std::max<int64_t>(0, hi - lo + 1);
+            lens[b] = sink_lens[b] + std::max<int64_t>(0, hi - lo + 1);
         }
         int64_t chunk;
         if (d.disable_split_kv) {
@@ -414,14 +486,15 @@ void build_schedule(const pkv_plan_desc &d, const std::vector<HostRequest> &reqs
                                        ? chunk
                                        : round_up((L + n - 1) / n, 16))
                                 : 0;
+            const int64_t sl = sink_lens[b];
+            std::vector<DecodePiece> pieces{{0, los[b], los[b]}};
             if (L > 0)
-                n = (L + per - 1) / per;
-            if (capturable && n > kCapturableMaxSplits) {
-                // the workspace of a capturable plan holds this many splits per request
-                n = kCapturableMaxSplits;
-                per = round_up((L + n - 1) / n, 16);
-                n = (L + per - 1) / per;
-            }
+                pieces = cut_pieces(sl, los[b], L - sl, per);
+            // the workspace of a capturable plan holds this many splits per request (a
+            // piece cut at the end of the sinks is one more)
+            for (int k = kCapturableMaxSplits; capturable && (int)pieces.size() > kCapturableMaxSplits; --k)
+                pieces = cut_pieces(sl, los[b], L - sl, round_up((L + k - 1) / k, 16));
+            n = (int64_t)pieces.size();
             int32_t pbase = -1, cbase = -1;
             if (n > 1) {
                 pbase = num_partials;
@@ -430,23 +503,23 @@ void build_schedule(const pkv_plan_desc &d, const std::vector<HostRequest> &reqs
                 num_counters += d.num_kv_heads * head_blocks;
             }
             for (int64_t s = 0; s < n; ++s) {
-                int64_t j0 = los[b] + s * per;
-                int64_t j1 = L > 0 ? std::min(los[b] + L, j0 + per) : j0;
+                const DecodePiece &pc = pieces[s];
                 for (int hk = 0; hk < d.num_kv_heads; ++hk)
                     for (int h0 = 0; h0 < group; h0 += kDecodeRows)
                         d_items.push_back({b, hk, hk * group + h0, std::min(kDecodeRows, group - h0),
-                                           (int32_t)j0, (int32_t)j1, n > 1 ? (int32_t)(pbase + s) : -1,
+                                           (int32_t)pc.j0, (int32_t)pc.j1, n > 1 ? (int32_t)(pbase + s) : -1,
                                            pbase, (int32_t)n,
                                            n > 1 ? cbase + hk * head_blocks + h0 / kDecodeRows : -1,
-                                           h_reqs[b].qo_begin, h_reqs[b].kv_len, h_reqs[b].kv_page_begin, 0});
+                                           h_reqs[b].qo_begin, h_reqs[b].kv_len, h_reqs[b].kv_page_begin,
+                                           (int32_t)pc.sink_end});
             }
         }
-        std::stable_sort(d_items.begin(), d_items.end(), [](const DecodeItem &a, const DecodeItem &b) {
-            return (a.j1 - a.j0) > (b.j1 - b.j0);
-        });
+        auto keys = [](const DecodeItem &it) { return it.sink_end + it.j1 - it.j0; };
+        std::stable_sort(d_items.begin(), d_items.end(),
+                         [&](const DecodeItem &a, const DecodeItem &b) { return keys(a) > keys(b); });
         decode_tile = fixed_tile > 0 ? fixed_tile
                                      : decode_tile_for(d.head_dim,
-                                                       d_items.empty() ? 0 : d_items.front().j1 - d_items.front().j0,
+                                                       d_items.empty() ? 0 : keys(d_items.front()),
                                                        (int64_t)d_items.size(), device_sm_count(device));
     }
     sc.num_partials = num_partials;
@@ -562,7 +635,8 @@ int pkv_abi_version(void) { return PKV_ABI_VERSION; }
 
 namespace {
 
-int create_plan(pkv_plan **out, const pkv_plan_desc *desc, const pkv_plan_caps *capacity, void *stream_)
+int create_plan(pkv_plan **out, const pkv_plan_desc *desc, const pkv_plan_caps *capacity, int32_t num_sinks,
+                void *stream_)
 {
     g_last_error.clear();
     if (!out)
@@ -573,6 +647,12 @@ int create_plan(pkv_plan **out, const pkv_plan_desc *desc, const pkv_plan_caps *
     if (st != PKV_OK)
         return st;
     const pkv_plan_desc &d = *desc;
+    if (num_sinks < 0)
+        return fail(PKV_ERR_INVALID_ARG, "num_sinks %d < 0", num_sinks);
+    if (num_sinks > kMaxSinks)
+        return fail(PKV_ERR_UNSUPPORTED, "num_sinks %d exceeds %d", num_sinks, kMaxSinks);
+    // without a window nothing is hidden from the sinks' queries: a plain plan
+    const int sinks = d.window_left < 0 ? 0 : num_sinks;
     const bool capturable = capacity != nullptr;
     if (capturable && d.kind == PKV_PREFILL_RAGGED)
         return fail(PKV_ERR_UNSUPPORTED, "ragged plans are not capturable (the K/V row count is baked into a launch)");
@@ -588,7 +668,7 @@ int create_plan(pkv_plan **out, const pkv_plan_desc *desc, const pkv_plan_caps *
     const int n_sm = device_sm_count(device);
 
     Schedule sc;
-    build_schedule(d, reqs, device, capturable, 0, sc);
+    build_schedule(d, reqs, device, capturable, 0, sinks, sc);
     const Caps caps = capturable ? caps_for_capacity(d, *capacity, n_sm) : caps_of(d, sc);
     if (capturable && (sc.total_q > caps.total_q))
         return fail(PKV_ERR_UNSUPPORTED, "the batch has %lld query rows, the capacity %lld",
@@ -639,6 +719,7 @@ int create_plan(pkv_plan **out, const pkv_plan_desc *desc, const pkv_plan_caps *
     plan->n_sm = n_sm;
     plan->capturable = capturable;
     plan->mask_mode = sc.mask_mode;
+    plan->sinks = sinks;
     plan->num_items = (int)(d.kind != PKV_DECODE ? sc.p_items.size() : sc.d_items.size());
     plan->num_partials = sc.num_partials;
     plan->num_ctas = sc.cta_items.empty() ? 0 : (int)sc.cta_items.size() - 1;
@@ -668,7 +749,14 @@ int create_plan(pkv_plan **out, const pkv_plan_desc *desc, const pkv_plan_caps *
 int pkv_plan_create(pkv_plan **out, const pkv_plan_desc *desc, void *stream)
 {
     NvtxRange range("pkv_plan_create");
-    return create_plan(out, desc, nullptr, stream);
+    return create_plan(out, desc, nullptr, 0, stream);
+}
+
+int pkv_plan_create_sinks(pkv_plan **out, const pkv_plan_desc *desc, int32_t num_sinks, const pkv_plan_caps *caps,
+                          void *stream)
+{
+    NvtxRange range("pkv_plan_create_sinks");
+    return create_plan(out, desc, caps, num_sinks, stream);
 }
 
 int pkv_plan_create_capturable(pkv_plan **out, const pkv_plan_desc *desc, const pkv_plan_caps *caps,
@@ -681,7 +769,7 @@ int pkv_plan_create_capturable(pkv_plan **out, const pkv_plan_desc *desc, const 
             *out = nullptr;
         return fail(PKV_ERR_INVALID_ARG, "caps is NULL");
     }
-    return create_plan(out, desc, caps, stream);
+    return create_plan(out, desc, caps, 0, stream);
 }
 
 int pkv_plan_update(pkv_plan *plan, const pkv_plan_desc *desc, void *stream_)
@@ -716,7 +804,7 @@ int pkv_plan_update(pkv_plan *plan, const pkv_plan_desc *desc, void *stream_)
     if (cudaGetDevice(&cur) != cudaSuccess || cur != plan->device)
         return fail(PKV_ERR_INVALID_ARG, "plan was made on device %d, current device is %d", plan->device, cur);
     Schedule sc;
-    build_schedule(d, reqs, plan->device, true, plan->decode_tile, sc);
+    build_schedule(d, reqs, plan->device, true, plan->decode_tile, plan->sinks, sc);
     const int64_t items = d.kind != PKV_DECODE ? (int64_t)sc.p_items.size() : (int64_t)sc.d_items.size();
     if (sc.total_q > plan->cap_total_q || items > plan->cap_items)
         return fail(PKV_ERR_UNSUPPORTED, "the batch needs %lld query rows and %lld work items, the capacity is %lld "
@@ -877,6 +965,7 @@ int pkv_run(const pkv_plan *plan, const void *q, const void *k_cache, const void
         p.v_scale = lf.v_scale;
         p.kv_dtype = d.kv_dtype;
         p.wait_probe = d.wait_probe;
+        p.sinks = plan->sinks > 0;
         p.wait_ns = wait_ns_of(d);
         if (plan->ev_begin && (ce = cudaEventRecord(plan->ev_begin, stream)) != cudaSuccess)
             return cuda_fail(ce, "cudaEventRecord");
@@ -908,6 +997,7 @@ int pkv_run(const pkv_plan *plan, const void *q, const void *k_cache, const void
     p.page_shift = page_shift_of(d.page_size);
     p.num_pages = d.num_pages;
     p.window_left = d.window_left;
+    p.sinks = plan->sinks;
     const LogitFactors lf = logit_factors(d);
     p.sm_scale_log2 = lf.sm_scale_log2;
     p.cap_in = lf.cap_in;

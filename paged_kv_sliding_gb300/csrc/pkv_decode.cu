@@ -1,6 +1,7 @@
 // Paged decode: host launch of the kernels in pkv_decode_kernel.cuh. This unit
 // instantiates the bf16-cache kernels and dispatches the 8-bit ones to
-// pkv_decode_fp8.cu (two units, so the build compiles them in parallel).
+// pkv_decode_fp8.cu and the ones with sinks to pkv_decode_sinks.cu (several units, so
+// the build compiles them in parallel).
 #include "pkv_decode_kernel.cuh"
 
 namespace pkv {
@@ -61,7 +62,6 @@ bool decode_tma_page_size(int page_size, int tile)
 cudaError_t launch_decode(const DecodeParams &p, int head_dim, int num_items, cudaStream_t s, int tile,
                           bool overlap_prev)
 {
-    using dec::launch_decode_dt;
     if (tile == 32 && head_dim > 128)
         return cudaErrorInvalidValue;
     const int tt = decode_kernel_tile(tile, head_dim, p.kv_dtype);
@@ -73,27 +73,11 @@ cudaError_t launch_decode(const DecodeParams &p, int head_dim, int num_items, cu
             !encode_kv_map(&tv, p.v_cache, head_dim, p.num_kv_heads, p.page_size, p.num_pages, rows, p.kv_dtype))
             return cudaErrorInvalidValue;
     }
+    if (p.sinks)
+        return launch_decode_sinks(p, head_dim, num_items, s, tile, tma, tk, tv, overlap_prev);
     if (p.kv_dtype != PKV_BF16)
         return launch_decode_kv8(p, head_dim, num_items, s, tile, tma, tk, tv, overlap_prev);
-    constexpr int BF = PKV_BF16;
-    if (tile == 32) {
-        switch (head_dim) {
-        case 64: return tma ? launch_decode_dt<64, true, 32, BF>(p, tk, tv, num_items, s, overlap_prev)
-                            : launch_decode_dt<64, false, 32, BF>(p, tk, tv, num_items, s, overlap_prev);
-        case 128: return tma ? launch_decode_dt<128, true, 32, BF>(p, tk, tv, num_items, s, overlap_prev)
-                             : launch_decode_dt<128, false, 32, BF>(p, tk, tv, num_items, s, overlap_prev);
-        default: return cudaErrorInvalidValue;
-        }
-    }
-    switch (head_dim) {
-    case 64: return tma ? launch_decode_dt<64, true, 64, BF>(p, tk, tv, num_items, s, overlap_prev)
-                        : launch_decode_dt<64, false, 64, BF>(p, tk, tv, num_items, s, overlap_prev);
-    case 128: return tma ? launch_decode_dt<128, true, 64, BF>(p, tk, tv, num_items, s, overlap_prev)
-                         : launch_decode_dt<128, false, 64, BF>(p, tk, tv, num_items, s, overlap_prev);
-    case 256: return tma ? launch_decode_dt<256, true, 64, BF>(p, tk, tv, num_items, s, overlap_prev)
-                         : launch_decode_dt<256, false, 64, BF>(p, tk, tv, num_items, s, overlap_prev);
-    default: return cudaErrorInvalidValue;
-    }
+    return dec::launch_decode_kv<PKV_BF16, false>(p, head_dim, num_items, s, tile, tma, tk, tv, overlap_prev);
 }
 
 }  // namespace pkv

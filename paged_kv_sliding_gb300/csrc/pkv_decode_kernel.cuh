@@ -27,6 +27,16 @@
 //     handles one split of a request writes an fp32 partial state; the group's
 //     last CTA to finish (an arrival counter after a memory fence) combines the
 //     partials through their LSE, so no second kernel runs.
+// Sinks (SINK): the item also sees the keys [0, sink_end), sink_end <= j0. The kernel
+// then walks a packed row index u: the loader-aligned pages (or, with cp.async, exactly
+// the rows) of the sinks, directly followed by those of [j0, j1), so that a few sinks
+// cost the stage they would fill and not one of their own:
+//     key(u) = u < join ? u : u + shift,
+//     join = min(round_up(sink_end, A), base), base = round_down(j0, A), shift = base - join,
+// with A the rows a box must start at a multiple of (1 for cp.async). In u the visible
+// keys are [0, sink_end) and [j0 - shift, j1 - shift), and no page of the gap between
+// them is read.
+//
 // All waits are bounded (the plan's wait bound, 2 s by default); on expiry
 // PKV_ERR_TIMEOUT is recorded and the CTA winds down after its outstanding copies
 // have landed.
@@ -119,7 +129,7 @@ __device__ __forceinline__ void fp8x4_pairs_to_f16x2(uint32_t w, uint32_t &even,
     }
 }
 
-template <int D, bool TMA_KV, int TT, int KV, int TPW>
+template <int D, bool TMA_KV, int TT, int KV, int TPW, bool SINK>
 __global__ void __launch_bounds__(DecTraits<D, TT, KV, TPW>::kThreads, DecTraits<D, TT, KV, TPW>::kMinBlocks)
     decode_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tm_k,
                   const __grid_constant__ CUtensorMap tm_v)
@@ -154,8 +164,23 @@ __global__ void __launch_bounds__(DecTraits<D, TT, KV, TPW>::kThreads, DecTraits
     struct {
         int32_t qo_begin, kv_len, kv_page_begin;
     } const rq = {it.row, it.kv_len, it.kv_page_begin};
-    const int tb = it.j1 > it.j0 ? (it.j0 / TT) * TT : it.j0;  // first tile start (64-aligned)
-    const int ntiles = it.j1 > it.j0 ? (it.j1 - tb + TT - 1) / TT : 0;
+    // The packed rows (SINK): visible ones [0, u_sink) and [u_lo, u_hi). Without sinks u
+    // is the key itself and the first tile starts at a multiple of TT.
+    int u_sink = 0, u_lo = it.j0, u_hi = it.j1, join = 0, shift = 0;
+    if (SINK) {
+        const int A = !TMA_KV ? 1 : (p.page_size < TT ? p.page_size : TT);
+        const int base = it.j0 / A * A;
+        u_sink = it.sink_end;
+        join = min((u_sink + A - 1) / A * A, base);
+        shift = base - join;
+        u_lo = it.j0 - shift;
+        u_hi = it.j1 - shift;
+    }
+    auto key_of = [&](int u) { return SINK && u >= join ? u + shift : u; };
+    auto visible = [&](int u) { return (u >= u_lo && u < u_hi) || (SINK && u < u_sink); };
+    // (with sinks an item always sees a key: the plan gives the others to plain ranges)
+    const int tb = SINK ? 0 : (it.j1 > it.j0 ? (it.j0 / TT) * TT : it.j0);  // first tile start
+    const int ntiles = it.j1 > it.j0 ? (u_hi - tb + TT - 1) / TT : 0;
     const volatile int *abort_v = &abort_flag;
 
     if (tid == 0) {
@@ -187,10 +212,17 @@ __global__ void __launch_bounds__(DecTraits<D, TT, KV, TPW>::kThreads, DecTraits
                 if (lane >= npg)
                     return -1;
                 const int ts = tb + t * TT;
-                const int lp = P <= TT ? ts / P + lane : ts / P;
-                const int first = P <= TT ? lp * P : ts;
-                // pages holding no key of [j0, j1) are not loaded
-                if (lp >= n_pages_req || first >= it.j1 || first + rows_box <= it.j0)
+                int lp, first;  // logical page and first (packed) row of the box
+                if (SINK) {
+                    first = P <= TT ? ts + lane * P : ts;
+                    lp = key_of(first) / P;
+                } else {
+                    lp = P <= TT ? ts / P + lane : ts / P;
+                    first = P <= TT ? lp * P : ts;
+                }
+                // pages holding no visible key are not loaded
+                if (lp >= n_pages_req ||
+                    ((first >= u_hi || first + rows_box <= u_lo) && !(SINK && first < u_sink)))
                     return -1;
                 const int pg = __ldg(p.kv_indices + rq.kv_page_begin + lp);
                 if ((unsigned)pg >= (unsigned)p.num_pages) {
@@ -214,7 +246,7 @@ __global__ void __launch_bounds__(DecTraits<D, TT, KV, TPW>::kThreads, DecTraits
                         break;
                 }
                 const int ts = tb + t * TT;
-                const int slot0 = P > TT ? ts % P : 0;
+                const int slot0 = P > TT ? key_of(ts) % P : 0;
                 const unsigned valid = __ballot_sync(0xffffffffu, pg >= 0);
                 if (lane == 0)
                     mbar_arrive_expect_tx(smem_u32(&full_bar[s]),
@@ -259,10 +291,10 @@ __global__ void __launch_bounds__(DecTraits<D, TT, KV, TPW>::kThreads, DecTraits
 #pragma unroll
                 for (int rr = 0; rr < TT / 32; ++rr) {
                     const int row = lane + 32 * rr;
-                    const int j = ts + row;
+                    const int j = key_of(ts + row);
                     size_t off = 0;
                     uint32_t bytes = 0;
-                    if (j >= it.j0 && j < it.j1) {
+                    if (visible(ts + row)) {
                         const int lp = p.page_shift >= 0 ? (j >> p.page_shift) : j / P;
                         const int page = __ldg(p.kv_indices + rq.kv_page_begin + lp);
                         if ((unsigned)page < (unsigned)p.num_pages) {
@@ -375,15 +407,14 @@ __global__ void __launch_bounds__(DecTraits<D, TT, KV, TPW>::kThreads, DecTraits
             const uint32_t kb = ring + s * Tr::kStageBytes;
             const uint32_t vb = kb + Tr::kTileBytes;
             const int wt0 = tb + t * TT + warp * TPW;  // first token of this warp's TPW
-            const bool partial = wt0 < it.j0 || wt0 + TPW > it.j1;
+            const bool partial = (wt0 < u_lo || wt0 + TPW > u_hi) && !(SINK && wt0 + TPW <= u_sink);
             if (TMA_KV && partial) {
-                // V rows outside [j0, j1) hold other keys, foreign slots or stale
+                // V rows that are not visible hold other keys, foreign slots or stale
                 // data: zero them so that P = 0 never meets a non-finite value.
                 uint8_t *vgen = ring_gen + s * Tr::kStageBytes + Tr::kTileBytes;
                 for (int e = lane; e < TPW * Tr::kGran; e += 32) {
                     const int row = warp * TPW + e / Tr::kGran, c = e % Tr::kGran;
-                    const int j = tb + t * TT + row;
-                    if (j < it.j0 || j >= it.j1)
+                    if (!visible(tb + t * TT + row))
                         *reinterpret_cast<uint4 *>(vgen + plane_off<TT, PR, GM>(row, c)) = make_uint4(0, 0, 0, 0);
                 }
                 __syncwarp();
@@ -461,8 +492,7 @@ __global__ void __launch_bounds__(DecTraits<D, TT, KV, TPW>::kThreads, DecTraits
                     for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            const int j = tok_base + nt * 8 + (e & 1);
-                            if (j < it.j0 || j >= it.j1)
+                            if (!visible(tok_base + nt * 8 + (e & 1)))
                                 sc[b][nt][e] = -INFINITY;
                         }
                 }
@@ -730,14 +760,14 @@ __global__ void __launch_bounds__(DecTraits<D, TT, KV, TPW>::kThreads, DecTraits
     }
 }
 
-template <int D, bool TMA_KV, int TT, int KV, int TPW = 16>
+template <int D, bool TMA_KV, int TT, int KV, int TPW, bool SINK>
 cudaError_t launch_decode_dt(const DecodeParams &p, const CUtensorMap &tk, const CUtensorMap &tv, int num_items,
                              cudaStream_t s, bool overlap_prev)
 {
     using Tr = DecTraits<D, TT, KV, TPW>;
     static bool configured = false;
     if (!configured) {
-        cudaError_t e = cudaFuncSetAttribute(decode_kernel<D, TMA_KV, TT, KV, TPW>,
+        cudaError_t e = cudaFuncSetAttribute(decode_kernel<D, TMA_KV, TT, KV, TPW, SINK>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, Tr::kDynSmem);
         if (e != cudaSuccess)
             return e;
@@ -757,7 +787,38 @@ cudaError_t launch_decode_dt(const DecodeParams &p, const CUtensorMap &tk, const
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = overlap_prev ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, decode_kernel<D, TMA_KV, TT, KV, TPW>, p, tk, tv);
+    return cudaLaunchKernelEx(&cfg, decode_kernel<D, TMA_KV, TT, KV, TPW, SINK>, p, tk, tv);
+}
+
+template <int D, int TT, int KV, int TPW, bool SINK>
+cudaError_t launch_decode_d(const DecodeParams &p, bool tma, const CUtensorMap &tk, const CUtensorMap &tv,
+                            int num_items, cudaStream_t s, bool overlap_prev)
+{
+    return tma ? launch_decode_dt<D, true, TT, KV, TPW, SINK>(p, tk, tv, num_items, s, overlap_prev)
+               : launch_decode_dt<D, false, TT, KV, TPW, SINK>(p, tk, tv, num_items, s, overlap_prev);
+}
+
+// The kernels of one cache type by the plan's tile variant and head_dim.
+template <int KV, bool SINK>
+cudaError_t launch_decode_kv(const DecodeParams &p, int head_dim, int num_items, cudaStream_t s, int tile, bool tma,
+                             const CUtensorMap &tk, const CUtensorMap &tv, bool overlap_prev)
+{
+    // 8-bit caches at head_dim <= 128: stages of twice the tokens, two 16-token sub-blocks
+    // per compute warp (decode_kernel_tile)
+    constexpr int M = KV == PKV_BF16 ? 1 : 2, TPW = KV == PKV_BF16 ? 16 : 32;
+    if (tile == 32) {
+        switch (head_dim) {
+        case 64: return launch_decode_d<64, 32 * M, KV, TPW, SINK>(p, tma, tk, tv, num_items, s, overlap_prev);
+        case 128: return launch_decode_d<128, 32 * M, KV, TPW, SINK>(p, tma, tk, tv, num_items, s, overlap_prev);
+        default: return cudaErrorInvalidValue;
+        }
+    }
+    switch (head_dim) {
+    case 64: return launch_decode_d<64, 64 * M, KV, TPW, SINK>(p, tma, tk, tv, num_items, s, overlap_prev);
+    case 128: return launch_decode_d<128, 64 * M, KV, TPW, SINK>(p, tma, tk, tv, num_items, s, overlap_prev);
+    case 256: return launch_decode_d<256, 64, KV, 16, SINK>(p, tma, tk, tv, num_items, s, overlap_prev);
+    default: return cudaErrorInvalidValue;
+    }
 }
 
 }  // namespace dec

@@ -32,21 +32,31 @@ struct PrefillItem {
     int32_t kv_start;    // first key of the item's first KV tile (aligned for the loader)
     int32_t kv_tiles;    // KV tiles of the item (0: no visible key)
     int32_t kv_tile_rot; // tiles are visited from tile kv_tile_rot on, wrapping around
-    int32_t pad0;
+    int32_t join;        // plans with sinks: packed rows below it are the first keys themselves
 };
 
-// First key of the KV tile visited at step j (0 <= j < kv_tiles) of a prefill item
+// First row of the KV tile visited at step j (0 <= j < kv_tiles) of a prefill item
 // whose tiles hold T keys. Softmax accumulation is order-independent; staggering the
 // start keeps the items that run at the same time on one KV head from all missing L2
-// on the same tile.
-__host__ __device__ inline int prefill_kv_key_at(const PrefillItem &it, int j, int T)
+// on the same tile. Rows are keys, counted from the item's first key; in a plan with
+// sinks they are packed: the pages of the sinks, then directly those of the window.
+template <bool SINK = false>
+__host__ __device__ inline int prefill_kv_row_at(const PrefillItem &it, int j, int T)
 {
     const int k = j + it.kv_tile_rot;
-    return it.kv_start + (k < it.kv_tiles ? k : k - it.kv_tiles) * T;
+    return (SINK ? 0 : it.kv_start) + (k < it.kv_tiles ? k : k - it.kv_tiles) * T;
+}
+
+// The key of a row: rows at and above `join` lie kv_start keys further on (sinks).
+template <bool SINK = false>
+__host__ __device__ inline int prefill_row_key(const PrefillItem &it, int row)
+{
+    return SINK && row >= it.join ? row + it.kv_start : row;
 }
 
 // One CTA of the decode kernel: up to kDecodeRows query heads of one request's
-// single row against the key range [j0, j1) of one KV head.
+// single row against the key range [j0, j1) of one KV head (and, in a plan with sinks,
+// the first keys [0, sink_end) before it).
 struct DecodeItem {
     int32_t req;
     int32_t kv_head;
@@ -62,7 +72,7 @@ struct DecodeItem {
     int32_t row;            // the request's query row (its qo_begin)
     int32_t kv_len;         // keys in the request's cache
     int32_t kv_page_begin;  // the request's first entry in kv_indices
-    int32_t pad0;
+    int32_t sink_end;       // keys [0, sink_end) are visible too (sink plans; <= j0)
 };
 
 // Merge of a request's split-KV partial states into its output row.
@@ -76,7 +86,14 @@ struct MergeItem {
 constexpr int kDecodeRows = 16;   // query heads per decode CTA (one m16 MMA tile)
 constexpr int kPrefillRows = 128; // packed query rows per prefill CTA (UMMA M)
 
-enum MaskMode : int32_t { kMaskNone = 0, kMaskCausal = 1, kMaskCausalWindow = 2, kMaskWindow = 3 };
+enum MaskMode : int32_t {
+    kMaskNone = 0,
+    kMaskCausal = 1,
+    kMaskCausalWindow = 2,
+    kMaskWindow = 3,
+    kMaskCausalWindowSinks = 4,
+    kMaskWindowSinks = 5
+};
 
 struct DecodeParams {
     const DecodeItem *items;
@@ -103,6 +120,7 @@ struct DecodeParams {
     float v_scale;       // multiplies the final output
     int32_t kv_dtype;    // element type of the caches (pkv_dtype: bf16 or an 8-bit float)
     int32_t wait_probe;  // nonzero: each CTA's first consuming wait is on a barrier nothing completes
+    int32_t sinks;       // nonzero: the items may see sinks (the kernels for two key ranges)
     long long wait_ns;   // bound of every wait (globaltimer nanoseconds)
 };
 
@@ -136,6 +154,7 @@ struct PrefillParams {
     int32_t page_shift;
     int32_t num_pages;
     int32_t window_left;
+    int32_t sinks;           // keys [0, sinks) stay visible under the window (0: none)
     int32_t total_q;         // rows of q (bound of the query tensor map)
     float sm_scale_log2;     // sm_scale * k_scale * log2(e)
     float cap_in;            // soft cap, as in DecodeParams
@@ -212,6 +231,9 @@ bool encode_kv_map(CUtensorMap *m, const void *base, int head_dim, int num_kv_he
 // The 8-bit-cache decode kernels (p.kv_dtype = PKV_FP8_E4M3 or PKV_FP8_E5M2).
 cudaError_t launch_decode_kv8(const DecodeParams &p, int head_dim, int num_items, cudaStream_t s, int tile,
                               bool tma, const CUtensorMap &tk, const CUtensorMap &tv, bool overlap_prev);
+// The decode kernels of plans with sinks, over any cache type.
+cudaError_t launch_decode_sinks(const DecodeParams &p, int head_dim, int num_items, cudaStream_t s, int tile,
+                                bool tma, const CUtensorMap &tk, const CUtensorMap &tv, bool overlap_prev);
 cudaError_t launch_merge_partials(const MergePartialsParams &p, int head_dim, cudaStream_t s);
 cudaError_t launch_merge_state(const void *v_a, const float *s_a, const void *v_b,
                                const float *s_b, void *v_out, float *s_out, int64_t rows,
@@ -224,6 +246,13 @@ bool prefill_pp_tma_page_size(int page_size, int head_dim);
 // The prefill kernels over 8-bit caches (p.kv_dtype = PKV_FP8_E4M3 or PKV_FP8_E5M2).
 cudaError_t launch_prefill_pp_kv8(const PrefillParams &p, int head_dim, int mask_mode, int num_ctas,
                                   cudaStream_t s);
+// The prefill kernels of plans with sinks (mask modes kMaskCausalWindowSinks and
+// kMaskWindowSinks): bf16 caches with the launch's tensor maps, and 8-bit caches.
+cudaError_t launch_prefill_pp_sinks(const PrefillParams &p, int head_dim, int mask_mode, bool tma_kv,
+                                    const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
+                                    const CUtensorMap &to, int num_ctas, cudaStream_t s);
+cudaError_t launch_prefill_pp_kv8_sinks(const PrefillParams &p, int head_dim, int mask_mode, int num_ctas,
+                                        cudaStream_t s);
 
 // Set the calling thread's pkv_last_error() text.
 void set_last_error(const char *msg);

@@ -1,5 +1,6 @@
 // Paged prefill / extend: host launch of the kernels in pkv_prefill_kernel.cuh (bf16
-// caches; the 8-bit-cache kernels are instantiated in pkv_prefill_fp8.cu).
+// caches; the 8-bit-cache kernels are instantiated in pkv_prefill_fp8.cu, those of plans
+// with sinks in pkv_prefill_sinks.cu and pkv_prefill_sinks_fp8.cu).
 #include "pkv_prefill_kernel.cuh"
 
 namespace pkv {
@@ -52,7 +53,8 @@ int prefill_kv_tile(int head_dim) { return head_dim >= 256 ? 64 : 128; }
 cudaError_t launch_prefill_pp(const PrefillParams &p, int head_dim, int mask_mode, int num_ctas, cudaStream_t s)
 {
     if (p.kv_dtype != PKV_BF16)
-        return launch_prefill_pp_kv8(p, head_dim, mask_mode, num_ctas, s);
+        return p.sinks > 0 ? launch_prefill_pp_kv8_sinks(p, head_dim, mask_mode, num_ctas, s)
+                           : launch_prefill_pp_kv8(p, head_dim, mask_mode, num_ctas, s);
     const int g = p.group, tq = p.tokens_per_tile, Hkv = p.num_kv_heads, P = p.page_size;
     const bool tma_kv = p.ragged || prefill_pp_tma_page_size(P, head_dim);
     const int T = prefill_kv_tile(head_dim);
@@ -78,6 +80,8 @@ cudaError_t launch_prefill_pp(const PrefillParams &p, int head_dim, int mask_mod
         const cuuint32_t box[4] = {64, 1, (cuuint32_t)T, 1};
         if (!encode_4d(&tm_k, p.k_cache, dims, strides, box) || !encode_4d(&tm_v, p.v_cache, dims, strides, box))
             return cudaErrorInvalidValue;
+        if (p.sinks > 0)
+            return launch_prefill_pp_sinks(p, head_dim, mask_mode, true, tm_q, tm_k, tm_v, tm_o, num_ctas, s);
         switch (head_dim) {
         case 64: return pp::launch_pp_dt<64, true, true, PKV_BF16>(p, mask_mode, tm_q, tm_k, tm_v, tm_o, num_ctas, s);
         case 128: return pp::launch_pp_dt<128, true, true, PKV_BF16>(p, mask_mode, tm_q, tm_k, tm_v, tm_o, num_ctas, s);
@@ -99,6 +103,8 @@ cudaError_t launch_prefill_pp(const PrefillParams &p, int head_dim, int mask_mod
         if (!encode_nd(&tm_k, 5, p.k_cache, dims, strides, box) || !encode_nd(&tm_v, 5, p.v_cache, dims, strides, box))
             return cudaErrorInvalidValue;
     }
+    if (p.sinks > 0)
+        return launch_prefill_pp_sinks(p, head_dim, mask_mode, tma_kv, tm_q, tm_k, tm_v, tm_o, num_ctas, s);
     switch (head_dim) {
     case 64:
         return tma_kv ? pp::launch_pp_dt<64, true, false, PKV_BF16>(p, mask_mode, tm_q, tm_k, tm_v, tm_o, num_ctas, s)

@@ -44,6 +44,13 @@
 // its own Q tile for the next item as f16 with every row scaled by a power of two
 // (max |q| * 2^e in [2^13, 2^14)) and scales that row's logits back by 2^-e; P goes to
 // the PV MMA as f16.
+//
+// Sinks (mask modes 4 and 5): the first keys stay visible under the window. An item's
+// KV tiles then walk packed rows: the pages of the sinks, directly followed by those of
+// its window, key(u) = u < join ? u : u + kv_start (the plan picks join and kv_start on
+// the loader's alignment), so the sinks cost the rows they fill and not a tile of their
+// own, and the gap between them and the window is never read. The mask of a row is the
+// union of two column ranges; tiles inside either take none, as without sinks.
 #pragma once
 
 #include <cfloat>
@@ -101,6 +108,12 @@ constexpr int kRegsSoftmax = 200;
 constexpr int kRegsOther = 96;
 static_assert(256 * kRegsSoftmax + 128 * kRegsOther <= 384 * kRegsLaunch, "register split");
 
+// The lowest n bits of a word (none for n <= 0, all for n >= 32).
+__device__ __forceinline__ uint32_t bits_below(int n)
+{
+    return n <= 0 ? 0u : (n >= 32 ? 0xffffffffu : (1u << n) - 1u);
+}
+
 template <int NS>
 struct PPBars {
     static constexpr int kQ = 0;
@@ -136,8 +149,9 @@ __global__ void __launch_bounds__(384, 1)
     constexpr int T = Tr::kT;
     constexpr int NCH = Tr::kNCh;
     constexpr int CH = D / 8;
-    constexpr bool kCausal = MASK == kMaskCausal || MASK == kMaskCausalWindow;
-    constexpr bool kWindow = MASK == kMaskCausalWindow || MASK == kMaskWindow;
+    constexpr bool kSink = MASK == kMaskCausalWindowSinks || MASK == kMaskWindowSinks;
+    constexpr bool kCausal = MASK == kMaskCausal || MASK == kMaskCausalWindow || MASK == kMaskCausalWindowSinks;
+    constexpr bool kWindow = MASK == kMaskCausalWindow || MASK == kMaskWindow || kSink;
     // One query tile per item (head_dim 256, bf16 caches): S is double-buffered in TMEM
     // (S(j+1) is computed while the softmax works on S(j)); the softmax warpgroup is 0.
     constexpr bool kDS = Tr::kNQ == 1 && !KV8;
@@ -271,10 +285,10 @@ __global__ void __launch_bounds__(384, 1)
                     c_j = 0;
                 }
                 if (c_ii < item_hi) {
-                    const int j0 = prefill_kv_key_at(c_it, c_j, T);
+                    const int j0 = prefill_kv_row_at<kSink>(c_it, c_j, T);
                     for (int t = pt; t < T; t += NP) {
                         int *dst = &id_ring[(n_ids % kIdRing) * Tr::kIdsPerTile + t];
-                        const int jj = j0 + t;
+                        const int jj = prefill_row_key<kSink>(c_it, j0 + t);
                         if (jj < c_kv_len) {
                             const int lp = p.page_shift >= 0 ? (jj >> p.page_shift) : jj / p.page_size;
                             cp_async_4(smem_u32(dst), p.kv_indices + c_page_begin + lp);
@@ -299,7 +313,7 @@ __global__ void __launch_bounds__(384, 1)
                 if (n_tiles <= 0)
                     continue;
                 for (int j = 0; okp && j < n_tiles; ++j, ++n_t) {
-                    const int j0 = prefill_kv_key_at(it, j, T);
+                    const int j0 = prefill_kv_row_at<kSink>(it, j, T);
                     sync_producers();  // every producer is done with the ring entry refilled next
                     fetch_ids();
                     cp_async_wait<kIdRing - 1>();
@@ -316,7 +330,7 @@ __global__ void __launch_bounds__(384, 1)
                         const uint16_t *src = isv ? p.v_cache : p.k_cache;
                         for (int u = pt; u < kUnits; u += NP) {
                             const int t = u / kUPR, q0 = (u % kUPR) * kGU;  // row, first granule
-                            const int jj = j0 + t;
+                            const int jj = prefill_row_key<kSink>(it, j0 + t);
                             const int page = ids[t];
                             size_t off = 0;
                             uint32_t bytes = 0;
@@ -512,6 +526,10 @@ __global__ void __launch_bounds__(384, 1)
                 const int pos = rq.q_start + tok;
                 const int p_min = rq.q_start + it.tok0 + wg * tq;
                 const int p_max = p_min + ntok_wg - 1;
+                // sinks: first window key of this row and of the tile's last row, sink keys
+                const int w_lo = kSink ? (int)max((long long)pos - p.window_left, 0LL) : 0;
+                const int w_lo_max = kSink ? (int)max((long long)p_max - p.window_left, 0LL) : 0;
+                const int n_sink = kSink ? min(p.sinks, rq.kv_len) : 0;
                 float m_used = -INFINITY;
                 float l = 0.f;
                 for (int j = 0; j < n_tiles; ++j, ++n_s) {
@@ -535,13 +553,38 @@ __global__ void __launch_bounds__(384, 1)
                             s[c] = p.cap_out * soft_cap_tanh(s[c] * cap_in);
                     }
 
-                    const int j0 = prefill_kv_key_at(it, j, T);
-                    bool need_mask = j0 + T > rq.kv_len;
-                    if (kCausal)
-                        need_mask |= j0 + T - 1 > p_min;
-                    if (kWindow)
-                        need_mask |= j0 < p_max - p.window_left;
-                    if (need_mask) {
+                    const int j0 = prefill_kv_row_at<kSink>(it, j, T);
+                    bool need_mask;
+                    if (kSink) {
+                        const int k0 = j0 + it.kv_start;  // key of row j0 above the join
+                        const bool in_window = j0 >= it.join && k0 >= w_lo_max && k0 + T <= rq.kv_len &&
+                                               (!kCausal || k0 + T - 1 <= p_min);
+                        const bool in_sinks = j0 + T <= n_sink && (j0 + T <= it.join || it.kv_start == 0) &&
+                                              (!kCausal || j0 + T - 1 <= p_min);
+                        need_mask = !(in_window || in_sinks);
+                    } else {
+                        need_mask = j0 + T > rq.kv_len;
+                        if (kCausal)
+                            need_mask |= j0 + T - 1 > p_min;
+                        if (kWindow)
+                            need_mask |= j0 < p_max - p.window_left;
+                    }
+                    if (kSink && need_mask) {
+                        const int lo_c = max(w_lo - it.kv_start, it.join) - j0;
+                        const int k_hi = kCausal ? min(rq.kv_len - 1, pos) : rq.kv_len - 1;
+                        const int hi_c = k_hi - it.kv_start - j0;
+                        const int sink_c = min(n_sink - 1, k_hi) - j0;
+                        // 32 columns at a time as a word of visible bits (two comparisons a
+                        // column cost the registers that hold the scores)
+    #pragma unroll
+                        for (int w = 0; w < T / 32; ++w) {
+                            const uint32_t vis = bits_below(sink_c + 1 - 32 * w) |
+                                                 (bits_below(hi_c + 1 - 32 * w) & ~bits_below(lo_c - 32 * w));
+    #pragma unroll
+                            for (int c = 0; c < 32; ++c)
+                                s[32 * w + c] = (vis >> c) & 1u ? s[32 * w + c] : -INFINITY;
+                        }
+                    } else if (need_mask) {
                         const int lo_c = kWindow ? pos - p.window_left - j0 : INT_MIN;
                         int hi_c = rq.kv_len - 1 - j0;
                         if (kCausal)
@@ -970,7 +1013,7 @@ __global__ void __launch_bounds__(384, 1)
                     continue;
                 const int row_base = p.reqs[it.req].kv_page_begin;
                 for (int j = 0; okp && j < n_tiles; ++j) {
-                    const int row0 = row_base + prefill_kv_key_at(it, j, T);
+                    const int row0 = row_base + prefill_row_key<kSink>(it, prefill_kv_row_at<kSink>(it, j, T));
                     const uint32_t full = bar(B::kFull + n % NS);  // K and V of the tile complete it
                     for (int isv = 0; isv < 2; ++isv, ++n) {
                         const int s = n % NS;
@@ -1031,8 +1074,10 @@ __global__ void __launch_bounds__(384, 1)
                 auto load_id = [&](int j) -> int {
                     if (lane >= npg)
                         return -1;
-                    const int j0 = prefill_kv_key_at(it, j, T);
-                    const int lp = P <= T ? j0 / P + lane : j0 / P;
+                    const int j0 = prefill_kv_row_at<kSink>(it, j, T);
+                    const int lp = kSink ? prefill_row_key<kSink>(it, P <= T ? j0 + lane * P : j0) / P
+                                   : P <= T ? j0 / P + lane
+                                            : j0 / P;
                     if (lp >= n_pages_req)
                         return -1;
                     const int pg = __ldg(p.kv_indices + rq.kv_page_begin + lp);
@@ -1043,17 +1088,19 @@ __global__ void __launch_bounds__(384, 1)
                     }
                     return pg;
                 };
+                // first row past the cache end
+                const int row_end = !kSink || rq.kv_len <= it.join ? rq.kv_len : max(it.join, rq.kv_len - it.kv_start);
                 int pg = load_id(0);
                 for (int j = 0; okp && j < n_tiles; ++j) {
-                    const int j0 = prefill_kv_key_at(it, j, T);
-                    const int slot0 = P > T ? j0 % P : 0;
+                    const int j0 = prefill_kv_row_at<kSink>(it, j, T);
+                    const int slot0 = P > T ? prefill_row_key<kSink>(it, j0) % P : 0;
                     int pg_next = -1;
                     // K, then V. Both complete the K slot's barrier; a V tile reaching
                     // past the cache end lands on warp 9's own barrier instead: its rows
                     // past the end hold stale or foreign data and are zeroed (so that
                     // P = 0 never meets a non-finite value) before warp 9's arrival
                     // completes the K slot's barrier.
-                    const bool tail = j0 + T > rq.kv_len;
+                    const bool tail = j0 + T > row_end;
                     const unsigned valid = __ballot_sync(0xffffffffu, pg >= 0);
                     const uint32_t bytes = (uint32_t)__popc(valid) * rows_box * Tr::kChunk * NCH;
                     const uint32_t full = bar(B::kFull + n % NS);
@@ -1092,7 +1139,7 @@ __global__ void __launch_bounds__(384, 1)
                             ++n_land;
                             if (!land_ok)
                                 continue;
-                            const int vr = max(0, rq.kv_len - j0);
+                            const int vr = max(0, row_end - j0);
                             const int n16 = (T - vr) * 8;  // 16-byte granules per chunk
                             for (int idx = lane; idx < n16 * NCH; idx += 32) {
                                 const int c = idx / n16, e = idx % n16;
@@ -1144,11 +1191,11 @@ __global__ void __launch_bounds__(384, 1)
         auto load_ids = [&](int ii, int j, int (&pg)[kUPT], int (&sl)[kUPT]) {
             const PrefillItem it = p.items[ii];
             const RequestInfo rq = p.reqs[it.req];
-            const int j0 = prefill_kv_key_at(it, j, T);
+            const int j0 = prefill_kv_row_at<kSink>(it, j, T);
 #pragma unroll
             for (int k = 0; k < kUPT; ++k) {
                 const int u = pt + k * NP;
-                const int jj = j0 + u % T;
+                const int jj = prefill_row_key<kSink>(it, j0 + u % T);
                 pg[k] = -1;
                 sl[k] = 0;
                 if (u < 2 * T && jj < rq.kv_len) {
@@ -1303,6 +1350,20 @@ cudaError_t launch_pp_dt(const PrefillParams &p, int mask_mode, const CUtensorMa
     case kMaskCausalWindow:
         return launch_pp_dmt<D, kMaskCausalWindow, TMA_KV, RAGGED, KV>(p, tq, tk, tv, to, num_ctas, s);
     case kMaskWindow: return launch_pp_dmt<D, kMaskWindow, TMA_KV, RAGGED, KV>(p, tq, tk, tv, to, num_ctas, s);
+    default: return cudaErrorInvalidValue;
+    }
+}
+
+// The same for the mask modes with sinks (instantiated in units of their own).
+template <int D, bool TMA_KV, bool RAGGED, int KV>
+cudaError_t launch_pp_dt_sinks(const PrefillParams &p, int mask_mode, const CUtensorMap &tq, const CUtensorMap &tk,
+                               const CUtensorMap &tv, const CUtensorMap &to, int num_ctas, cudaStream_t s)
+{
+    switch (mask_mode) {
+    case kMaskCausalWindowSinks:
+        return launch_pp_dmt<D, kMaskCausalWindowSinks, TMA_KV, RAGGED, KV>(p, tq, tk, tv, to, num_ctas, s);
+    case kMaskWindowSinks:
+        return launch_pp_dmt<D, kMaskWindowSinks, TMA_KV, RAGGED, KV>(p, tq, tk, tv, to, num_ctas, s);
     default: return cudaErrorInvalidValue;
     }
 }

@@ -43,7 +43,7 @@ EXPORTED = ("pkv_plan_create", "pkv_run", "pkv_merge_state", "pkv_plan_destroy",
             "pkv_plan_get_info", "pkv_plan_device_status", "pkv_status_string",
             "pkv_last_error", "pkv_abi_version", "pkv_plan_set_timing_events",
             "pkv_decode_noalloc", "pkv_plan_create_capturable", "pkv_plan_update",
-            "pkv_build_kv_indices")
+            "pkv_build_kv_indices", "pkv_plan_create_sinks")
 
 
 class PkvError(RuntimeError):
@@ -142,6 +142,9 @@ def load_library(path: Optional[str] = None):
         lib.pkv_plan_create_capturable.argtypes = [ctypes.POINTER(vp), ctypes.POINTER(PlanDesc),
                                                     ctypes.POINTER(PlanCaps), vp]
         lib.pkv_plan_create_capturable.restype = ctypes.c_int
+        lib.pkv_plan_create_sinks.argtypes = [ctypes.POINTER(vp), ctypes.POINTER(PlanDesc), i32,
+                                              ctypes.POINTER(PlanCaps), vp]
+        lib.pkv_plan_create_sinks.restype = ctypes.c_int
         lib.pkv_plan_update.argtypes = [vp, ctypes.POINTER(PlanDesc), vp]
         lib.pkv_plan_update.restype = ctypes.c_int
         lib.pkv_build_kv_indices.argtypes = [vp, i32, i64, vp, vp, vp, i32, vp, i64, vp, vp, i64, vp, vp]
@@ -190,7 +193,8 @@ class Plan:
                  sm_scale: Optional[float] = None, qo_indptr=None, q_start=None,
                  fixed_split_size: int = -1, disable_split_kv: bool = False, stream=None,
                  capacity: Optional[dict] = None, logits_soft_cap: float = 0.0, k_scale: float = 1.0,
-                 v_scale: float = 1.0, kv_dtype="bf16", wait_limit_us: int = 0, wait_probe: bool = False):
+                 v_scale: float = 1.0, kv_dtype="bf16", wait_limit_us: int = 0, wait_probe: bool = False,
+                 num_sinks: int = 0):
         """kind: "prefill", "decode" or "prefill_ragged" (K/V passed to run() are
         contiguous [total_kv, H_kv, d]; kv_indptr counts tokens; no page table).
         capacity={"max_batch": B, "max_total_q": Q}: a capturable plan (its run may
@@ -198,7 +202,8 @@ class Plan:
         kv_dtype: element type of the caches, "bf16", "e4m3" or "e5m2" (or the torch
         dtype); the 8-bit ones are for paged (decode and prefill) plans.
         wait_limit_us: bound of every device-side wait (<= 0: 2 s); wait_probe: make
-        each CTA's first consuming wait run out (tests of the timeout path)."""
+        each CTA's first consuming wait run out (tests of the timeout path).
+        num_sinks: first keys of each request that stay visible under the window."""
         self._lib = load_library()
         self._handle = ctypes.c_void_p()
         self.kind = kind
@@ -249,13 +254,19 @@ class Plan:
         d.wait_limit_us = int(wait_limit_us)
         d.wait_probe = 1 if wait_probe else 0
         self._desc = d
-        if capacity is None:
-            _check(self._lib.pkv_plan_create(ctypes.byref(self._handle), ctypes.byref(d),
-                                             _stream_handle(stream)), "pkv_plan_create")
-        else:
+        caps = None
+        if capacity is not None:
             caps = PlanCaps()
             caps.max_batch = int(capacity["max_batch"])
             caps.max_total_q = int(capacity.get("max_total_q", capacity["max_batch"]))
+        if num_sinks:
+            _check(self._lib.pkv_plan_create_sinks(ctypes.byref(self._handle), ctypes.byref(d), int(num_sinks),
+                                                   None if caps is None else ctypes.byref(caps),
+                                                   _stream_handle(stream)), "pkv_plan_create_sinks")
+        elif caps is None:
+            _check(self._lib.pkv_plan_create(ctypes.byref(self._handle), ctypes.byref(d),
+                                             _stream_handle(stream)), "pkv_plan_create")
+        else:
             _check(self._lib.pkv_plan_create_capturable(ctypes.byref(self._handle), ctypes.byref(d),
                                                         ctypes.byref(caps), _stream_handle(stream)),
                    "pkv_plan_create_capturable")

@@ -362,6 +362,57 @@ PKV_API int pkv_build_kv_indices(const int32_t *req_to_token, int32_t num_rows, 
                                  int32_t *kv_indptr, int32_t *kv_indices, int64_t kv_indices_capacity,
                                  int32_t *status, void *stream);
 
+/* Sizes and constants of pkv_norm_rope_append. */
+typedef struct pkv_append_desc {
+    int64_t num_tokens;
+    int64_t q_stride;        /* elements from a token's row to the next (multiples of 8), so that */
+    int64_t k_stride;        /* q, k and v may be slices of one projection's output; the heads    */
+    int64_t v_stride;        /* of a token are contiguous                                         */
+    int32_t num_qo_heads;    /* 0: no q */
+    int32_t num_kv_heads;    /* 0: no k and v */
+    int32_t head_dim;        /* 64, 128 or 256 */
+    int32_t page_size;       /* of the caches */
+    int32_t num_pages;
+    int32_t kv_dtype;        /* pkv_dtype of the caches: PKV_BF16, PKV_FP8_E4M3, PKV_FP8_E5M2 */
+    int32_t rotary_dim;      /* columns rotated: a multiple of 16 up to head_dim; 0: none */
+    int32_t interleaved;     /* pairs (2i, 2i + 1) (nonzero) or (i, i + rotary_dim / 2) */
+    int32_t max_position;    /* rows of cos_sin */
+    float eps;               /* added to the mean of the squares */
+    float weight_offset;     /* added to both weights (1 for weights stored around zero) */
+    float k_scale;           /* the caches hold k / k_scale and v / v_scale; <= 0 means 1 */
+    float v_scale;
+    int32_t reserved;
+} pkv_append_desc;
+
+/*
+ * pkv_norm_rope_append: what a layer does to its projections before pkv_run, in one pass.
+ * Every head of q and of k is normalised, then rotated by its token's position; q goes to
+ * q_out, k and v go into their slots of the paged caches (and k, if asked, to k_out):
+ *     y = x / sqrt(mean(x^2) + eps) * (weight + weight_offset)
+ *     (a, b) -> (a cos - b sin, b cos + a sin)  for the pairs of the first rotary_dim columns
+ *     k_cache[slot] = y / k_scale, v_cache[slot] = v / v_scale   (pkv_run multiplies them back)
+ * All in fp32 from the bf16 inputs, each result rounded once; 8-bit stores round to
+ * nearest even and keep to the format's finite range.
+ * DEVICE pointers: q [num_tokens, num_qo_heads, head_dim], k and v [num_tokens,
+ * num_kv_heads, head_dim] bf16 with the descriptor's token strides; q_weight, k_weight
+ * [head_dim] bf16, or NULL: that tensor is not normalised; cos_sin [max_position,
+ * rotary_dim] fp32, a position's cosines then its sines; positions [num_tokens] int32;
+ * slots [num_tokens] int64, page * page_size + slot in the page, or negative for a padding
+ * row, of which nothing is written; q_out, k_out contiguous bf16 (q_out may be q and k_out
+ * k where those are contiguous); caches as for pkv_run; status NULL or a device word that
+ * records PKV_ERR_DEVICE_BOUNDS for a slot beyond the caches or a position outside
+ * cos_sin, the row being skipped. The caches may both be NULL (k then goes to k_out alone,
+ * v is not read, slots may be NULL: every row is written), as may k_out. The tensors and
+ * caches are 16-byte aligned. Slots that are not negative must differ: of rows that share
+ * one, either may be what is left there.
+ * Asynchronous on `stream` (one launch), allocates nothing; capturable.
+ * Returns PKV_OK, PKV_ERR_INVALID_ARG, PKV_ERR_UNSUPPORTED or PKV_ERR_CUDA.
+ */
+PKV_API int pkv_norm_rope_append(const pkv_append_desc *desc, const void *q, const void *k, const void *v,
+                                 const void *q_weight, const void *k_weight, const float *cos_sin,
+                                 const int32_t *positions, const int64_t *slots, void *q_out, void *k_out,
+                                 void *k_cache, void *v_cache, int32_t *status, void *stream);
+
 /* PKV_ABI_VERSION of the loaded library. */
 PKV_API int pkv_abi_version(void);
 

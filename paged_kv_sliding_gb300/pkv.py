@@ -38,12 +38,13 @@ PKV_FP8_E5M2 = 3
 KV_DTYPES = {"bf16": PKV_BF16, "e4m3": PKV_FP8_E4M3, "e5m2": PKV_FP8_E5M2}
 _KV_TORCH = {PKV_BF16: torch.bfloat16, PKV_FP8_E4M3: torch.float8_e4m3fn,
              PKV_FP8_E5M2: torch.float8_e5m2}
+_KV_CODES = {v: k for k, v in _KV_TORCH.items()}
 
 EXPORTED = ("pkv_plan_create", "pkv_run", "pkv_merge_state", "pkv_plan_destroy",
             "pkv_plan_get_info", "pkv_plan_device_status", "pkv_status_string",
             "pkv_last_error", "pkv_abi_version", "pkv_plan_set_timing_events",
             "pkv_decode_noalloc", "pkv_plan_create_capturable", "pkv_plan_update",
-            "pkv_build_kv_indices", "pkv_plan_create_sinks")
+            "pkv_build_kv_indices", "pkv_plan_create_sinks", "pkv_norm_rope_append")
 
 
 class PkvError(RuntimeError):
@@ -86,6 +87,29 @@ class PlanCaps(ctypes.Structure):
         ("max_batch", ctypes.c_int32),
         ("reserved", ctypes.c_int32),
         ("max_total_q", ctypes.c_int64),
+    ]
+
+
+class AppendDesc(ctypes.Structure):
+    _fields_ = [
+        ("num_tokens", ctypes.c_int64),
+        ("q_stride", ctypes.c_int64),
+        ("k_stride", ctypes.c_int64),
+        ("v_stride", ctypes.c_int64),
+        ("num_qo_heads", ctypes.c_int32),
+        ("num_kv_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+        ("page_size", ctypes.c_int32),
+        ("num_pages", ctypes.c_int32),
+        ("kv_dtype", ctypes.c_int32),
+        ("rotary_dim", ctypes.c_int32),
+        ("interleaved", ctypes.c_int32),
+        ("max_position", ctypes.c_int32),
+        ("eps", ctypes.c_float),
+        ("weight_offset", ctypes.c_float),
+        ("k_scale", ctypes.c_float),
+        ("v_scale", ctypes.c_float),
+        ("reserved", ctypes.c_int32),
     ]
 
 
@@ -149,6 +173,8 @@ def load_library(path: Optional[str] = None):
         lib.pkv_plan_update.restype = ctypes.c_int
         lib.pkv_build_kv_indices.argtypes = [vp, i32, i64, vp, vp, vp, i32, vp, i64, vp, vp, i64, vp, vp]
         lib.pkv_build_kv_indices.restype = ctypes.c_int
+        lib.pkv_norm_rope_append.argtypes = [ctypes.POINTER(AppendDesc)] + [vp] * 14
+        lib.pkv_norm_rope_append.restype = ctypes.c_int
         lib.pkv_abi_version.argtypes = []
         lib.pkv_abi_version.restype = ctypes.c_int
         _lib = lib
@@ -364,6 +390,101 @@ def build_kv_indices(req_to_token: torch.Tensor, req_pool_indices: torch.Tensor,
                                     0 if loc_map is None else loc_map.numel(), _ptr(kv_indptr), _ptr(kv_indices),
                                     cap, _ptr(status), _stream_handle(stream)), "pkv_build_kv_indices")
     return kv_indptr, kv_indices
+
+
+def _rows(t: torch.Tensor, name: str):
+    """[tokens, heads, d] bf16 on the device whose heads are contiguous within a token."""
+    n, h, d = t.shape
+    if t.dtype != torch.bfloat16 or not t.is_cuda or (t.numel() and (t.stride(2) != 1 or (h > 1 and t.stride(1) != d))):
+        raise ValueError(f"{name} must be a CUDA bf16 tensor [tokens, heads, d] with contiguous heads")
+    return n, h, d, t.stride(0) if n > 1 else h * d
+
+
+def _want(t: Optional[torch.Tensor], name: str, dtype, shape=None):
+    if t is not None and (t.dtype != dtype or not t.is_cuda or not t.is_contiguous() or
+                          (shape is not None and tuple(t.shape) != tuple(shape))):
+        raise ValueError(f"{name} must be a contiguous CUDA {dtype} tensor" + (f" of shape {tuple(shape)}" if shape else ""))
+
+
+def _here(*tensors):
+    """The tensors live on the current device, whose stream the call is launched on."""
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.device.index != dev:
+            raise ValueError(f"a tensor on {t.device}, but the current device is cuda:{dev}")
+
+
+def norm_rope_append(q: Optional[torch.Tensor], k: Optional[torch.Tensor], v: Optional[torch.Tensor] = None, *,
+                     positions: Optional[torch.Tensor] = None, cos_sin: Optional[torch.Tensor] = None,
+                     slots: Optional[torch.Tensor] = None, k_cache: Optional[torch.Tensor] = None,
+                     v_cache: Optional[torch.Tensor] = None, q_weight: Optional[torch.Tensor] = None,
+                     k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6, weight_offset: float = 0.0,
+                     interleaved: bool = False, k_scale: float = 1.0, v_scale: float = 1.0,
+                     q_out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None,
+                     status: Optional[torch.Tensor] = None, stream=None):
+    """Normalise each head of q and k, rotate them by their tokens' positions and write k
+    and v into the paged caches, in one pass; returns q_out (None without q).
+
+    q [n, H_qo, d], k and v [n, H_kv, d] bf16, possibly slices of one projection (heads
+    contiguous, any token stride); q_weight / k_weight [d] bf16 (None: no norm); cos_sin
+    [max_position, rotary_dim] fp32 (cosines, then sines; None: no rotation); positions
+    [n] int32; slots [n] int64 (page * page_size + offset; negative: a padding row, not
+    written); caches [num_pages, P, H_kv, d] bf16, float8_e4m3fn or float8_e5m2, or both
+    None with k_out [n, H_kv, d]. status: device int32 word for out-of-range slots and
+    positions."""
+    lib = _lib or load_library()
+    d = AppendDesc()
+    n = dim = None
+    for t, name in ((q, "q"), (k, "k"), (v, "v")):
+        if t is None:
+            continue
+        tn, heads, td, stride = _rows(t, name)
+        if n is not None and (tn != n or td != dim):
+            raise ValueError("q, k and v must agree in tokens and head_dim")
+        n, dim = tn, td
+        setattr(d, name + "_stride", stride)
+        if name == "q":
+            d.num_qo_heads = heads
+        elif name == "k":
+            d.num_kv_heads = heads
+        elif k is None or heads != d.num_kv_heads:
+            raise ValueError("k and v must have the same heads")
+    if n is None:
+        raise ValueError("q or k is required")
+    d.num_tokens, d.head_dim = n, dim
+    _want(positions, "positions", torch.int32, (n,))
+    _want(slots, "slots", torch.int64, (n,))
+    _want(q_weight, "q_weight", torch.bfloat16, (dim,))
+    _want(k_weight, "k_weight", torch.bfloat16, (dim,))
+    _want(status, "status", torch.int32)
+    if cos_sin is not None:
+        _want(cos_sin, "cos_sin", torch.float32)
+        d.max_position, d.rotary_dim = cos_sin.shape
+        if positions is None:
+            raise ValueError("cos_sin needs positions")
+    if k_cache is not None or v_cache is not None:
+        if k_cache is None or v_cache is None or slots is None or v is None:
+            raise ValueError("k_cache, v_cache, v and slots come together")
+        code = _KV_CODES.get(k_cache.dtype)
+        if code is None or k_cache.dim() != 4 or tuple(k_cache.shape[2:]) != (d.num_kv_heads, dim):
+            raise ValueError("k_cache must be [num_pages, page_size, H_kv, d], bf16 or 8-bit")
+        _want(k_cache, "k_cache", k_cache.dtype)
+        _want(v_cache, "v_cache", k_cache.dtype, k_cache.shape)
+        d.num_pages, d.page_size, d.kv_dtype = k_cache.shape[0], k_cache.shape[1], code
+    if q is not None and q_out is None:
+        q_out = torch.empty((n, d.num_qo_heads, dim), dtype=torch.bfloat16, device=q.device)
+    if q is not None:
+        _want(q_out, "q_out", torch.bfloat16, (n, d.num_qo_heads, dim))
+    if k is not None:
+        _want(k_out, "k_out", torch.bfloat16, (n, d.num_kv_heads, dim))
+    _here(q, k, v, positions, cos_sin, slots, k_cache, v_cache, q_weight, k_weight, q_out, k_out, status)
+    d.eps, d.weight_offset, d.interleaved = eps, weight_offset, 1 if interleaved else 0
+    d.k_scale, d.v_scale = k_scale, v_scale
+    _check(lib.pkv_norm_rope_append(ctypes.byref(d), _ptr(q), _ptr(k), _ptr(v), _ptr(q_weight), _ptr(k_weight),
+                                    _ptr(cos_sin), _ptr(positions), _ptr(slots), _ptr(q_out), _ptr(k_out),
+                                    _ptr(k_cache), _ptr(v_cache), _ptr(status), _stream_handle(stream)),
+           "pkv_norm_rope_append")
+    return q_out
 
 
 def plan(**kw) -> Plan:

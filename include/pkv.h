@@ -413,6 +413,85 @@ PKV_API int pkv_norm_rope_append(const pkv_append_desc *desc, const void *q, con
                                  const int32_t *positions, const int64_t *slots, void *q_out, void *k_out,
                                  void *k_cache, void *v_cache, int32_t *status, void *stream);
 
+/*
+ * The pages of a cache, kept on the device. A pool is a page table of requests ("rows"),
+ * their lengths, and how many table entries in use name each page; a page is free iff
+ * that count is 0. An empty pool is lens = 0, refs = 0. Requests, the calls below and
+ * pkv_build_kv_indices (over table, with ceil(len / page_size) as kv_lens) share it.
+ * All pointers are DEVICE memory owned by the caller.
+ */
+typedef struct pkv_page_pool {
+    int32_t *table;          /* [num_rows, row_stride]; row r uses its first ceil(lens[r] / page_size) */
+    int32_t *lens;           /* [num_rows] tokens */
+    int32_t *refs;           /* [num_pages], 16-byte aligned */
+    int64_t row_stride;      /* pages a row can hold */
+    int32_t num_rows;
+    int32_t num_pages;
+    int32_t page_size;
+    int32_t reserved;
+    void *workspace;         /* pkv_pages_workspace bytes, 16-byte aligned, contents of no interest; */
+    int64_t workspace_bytes; /* calls that share one (captured graphs too) must not overlap          */
+    int32_t *status;         /* device word, required: see below */
+} pkv_page_pool;
+
+/* Bytes of a pool's workspace. */
+PKV_API int pkv_pages_workspace(int32_t num_rows, int32_t num_pages, int64_t *bytes);
+
+/*
+ * Every result of the calls below is a function of their inputs alone: new pages are the
+ * lowest free ids, handed out in the order of the call's entries and, within one, of its
+ * pages. A call whose inputs do not fit changes nothing but its outputs, which it fills
+ * with -1 (a slot or page id that pkv_norm_rope_append and pkv_copy_pages skip), and
+ * records in pool->status PKV_ERR_OOM (not enough free pages) or PKV_ERR_DEVICE_BOUNDS (a
+ * row out of range or named twice, a negative count, a length or row beyond row_stride
+ * pages, a page id out of range or with refs 0 in a row that is read, slots beyond their
+ * capacity). Index arrays are DEVICE int32; n is at most num_rows. Asynchronous on
+ * `stream`, one launch each (compact: two), nothing is allocated; capturable. They return
+ * PKV_OK, PKV_ERR_INVALID_ARG, PKV_ERR_UNSUPPORTED (sizes near 2^31) or PKV_ERR_CUDA.
+ *
+ * pkv_pages_extend: rows[i] grows by add[i] tokens. slots (or NULL) gets, entry after
+ * entry, each new token's slot page * page_size + offset, slots_capacity at most.
+ */
+PKV_API int pkv_pages_extend(const pkv_page_pool *pool, const int32_t *rows, const int32_t *add, int32_t n,
+                             int64_t *slots, int64_t slots_capacity, void *stream);
+
+/*
+ * pkv_pages_fork: children[i], an empty row, becomes a copy of parents[i] (parents may
+ * repeat; all are read as they were before the call). Full pages are shared; a last page
+ * that is not full, which the rows go on writing, is given to the child as a new page:
+ * src[i], dst[i] are the page to copy and its copy (pkv_copy_pages), or -1, -1.
+ */
+PKV_API int pkv_pages_fork(const pkv_page_pool *pool, const int32_t *parents, const int32_t *children, int32_t n,
+                           int32_t *src, int32_t *dst, void *stream);
+
+/* pkv_pages_free: the rows become empty; pages that no other row names are free again. */
+PKV_API int pkv_pages_free(const pkv_page_pool *pool, const int32_t *rows, int32_t n, void *stream);
+
+/*
+ * pkv_pages_compact: with n pages in use, the pages in use with ids from n on move to the
+ * free ids below n, both in ascending order, so that the first n pages of the caches hold
+ * everything. Writes the moves to src and dst (max_moves at most; num_pages / 2 always
+ * do), their number to *count (DEVICE), and the new table entries in use, lens and refs
+ * to `out`, whose arrays may be the pool's own (sizes equal, row_stride at least as
+ * large). More than max_moves moves: PKV_ERR_DEVICE_BOUNDS is recorded, nothing moves,
+ * *count is 0. The caller copies the pages (pkv_copy_pages with count) before it uses the
+ * new table, and src are free from then on.
+ */
+PKV_API int pkv_pages_compact(const pkv_page_pool *pool, const pkv_page_pool *out, int32_t *src, int32_t *dst,
+                              int32_t max_moves, int32_t *count, void *stream);
+
+/*
+ * pkv_copy_pages: page dst[i] of K and of V becomes page src[i], in each of num_layers
+ * caches of num_pages pages of page_bytes (a multiple of 16), layer_bytes apart. Pairs
+ * with a negative id are skipped, as are those from *count on (DEVICE; NULL: n); an id
+ * beyond the caches is recorded in status (DEVICE or NULL) and its pair skipped. No page
+ * may be a dst twice, or a dst and the src of another pair. Asynchronous on `stream`, one
+ * launch; capturable. Caches 16-byte aligned.
+ */
+PKV_API int pkv_copy_pages(void *k_cache, void *v_cache, int32_t num_layers, int64_t layer_bytes, int32_t num_pages,
+                           int64_t page_bytes, const int32_t *src, const int32_t *dst, int32_t n, const int32_t *count,
+                           int32_t *status, void *stream);
+
 /* PKV_ABI_VERSION of the loaded library. */
 PKV_API int pkv_abi_version(void);
 

@@ -24,7 +24,7 @@ LIB = os.path.join(PKG, "libpkv.so")
 SOURCES = ["pkv_api.cpp", "pkv_decode.cu", "pkv_decode_fp8.cu", "pkv_merge.cu", "pkv_prefill.cu",
            "pkv_prefill_fp8.cu",
            "pkv_noalloc.cu", "pkv_indices.cu", "pkv_decode_sinks.cu", "pkv_prefill_sinks.cu",
-           "pkv_prefill_sinks_fp8.cu", "pkv_append.cu"]
+           "pkv_prefill_sinks_fp8.cu", "pkv_append.cu", "pkv_pages.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -1,0 +1,866 @@
+// The pages of a cache, kept on the device: rows of a page table grow, fork, are freed and
+// packed together, and the pages themselves are copied, without a host round trip.
+//
+// State: table [num_rows, row_stride] page ids, lens [num_rows] tokens of a row (its first
+// ceil(len / P) entries are in use) and refs [num_pages], how many entries in use name a
+// page. A page is free iff its refs are 0, so nothing else has to be kept, and "the lowest
+// free ids, in the order of the call" makes every result a function of the inputs alone.
+//   extend: ceil((len + add) / P) - ceil(len / P) new pages for each row, slots of the tokens
+//   fork:   the child's row names the parent's full pages (refs + 1); a last page that is
+//           not full is one the child will write, so it gets a free one and (src, dst)
+//   free:   refs - 1 for the row's pages, len = 0
+//   compact: with n live pages, the live ids >= n move to the free ids < n, both ascending
+// A call that meets an input it cannot take (a row or page out of range, a row named twice,
+// not enough free pages) changes nothing and records why.
+//
+// extend, fork and free are one launch each of one cluster of 8 CTAs: the free pages have
+// to be ranked, a scan over refs, and the cluster's barriers and shared memories do in one
+// launch what would otherwise be three (count, scan, assign) or a scan of CTAs that spin on
+// one another. Every warp counts a segment of its own, the 256 counts are exchanged, and a
+// second pass over the segment (now in L2) writes the ids of the ranks that are wanted.
+// Bound by latency: four barriers' worth of dependent loads, over 4 bytes a page.
+#include <cooperative_groups.h>
+
+#include <string>
+
+#include "pkv_internal.h"
+#include "pkv_nvtx.h"
+#include "pkv_ptx.cuh"
+
+namespace pkv {
+namespace {
+
+namespace cg = cooperative_groups;
+
+constexpr int kCtas = 8;  // portable cluster size
+constexpr int kThreads = 1024;
+constexpr int kWarps = kThreads / 32;
+constexpr int kAllWarps = kCtas * kWarps;
+
+struct PoolParams {
+    int32_t *table, *lens, *refs;
+    int64_t row_stride;
+    int32_t num_rows, num_pages, page_size;
+    int32_t *status;
+    // workspace
+    int32_t *claim;      // [num_rows] entry of the call that named a row
+    int32_t *first;      // [num_rows] rank of an entry's first new page
+    int64_t *first_slot; // [num_rows] its first slot in the call's slots (fork: the parent's length,
+                         // which a child's may replace when a row is both)
+    int32_t *free_ids;   // [num_pages] the free pages by rank (compact: a page's rank)
+    int32_t *word;       // compact: the live pages
+};
+
+__device__ __forceinline__ int ceil_div(int64_t x, int p) { return (int)((x + p - 1) / p); }
+
+// What the CTAs of a cluster tell one another.
+struct Board {
+    int32_t pages[kWarps];   // by warp: new pages, free pages, new tokens of its segment
+    int32_t frees[kWarps];
+    long long tokens[kWarps];
+    int32_t error;
+    // every warp's, after the exchange
+    int32_t all_pages[kAllWarps];
+    int32_t all_frees[kAllWarps];
+    long long all_tokens[kAllWarps];
+};
+
+__device__ __forceinline__ int32_t warp_sum(int32_t x) { return __reduce_add_sync(0xffffffffu, x); }
+
+__device__ __forceinline__ long long warp_sum64(long long x)
+{
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1)
+        x += __shfl_xor_sync(0xffffffffu, x, o);
+    return x;
+}
+
+// Exclusive prefix over the lanes of a warp.
+__device__ __forceinline__ int warp_before(int x, int lane)
+{
+    int s = x;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, s, o);
+        if (lane >= o)
+            s += y;
+    }
+    return s - x;
+}
+
+__device__ __forceinline__ long long warp_before64(long long x, int lane)
+{
+    long long s = x;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, s, o);
+        if (lane >= o)
+            s += y;
+    }
+    return s - x;
+}
+
+// Segment of `n` items that warp gw of the cluster handles: [lo, hi), multiples of `unit`.
+__device__ __forceinline__ void segment(int n, int unit, int gw, int &lo, int &hi)
+{
+    const int per = ((n + kAllWarps - 1) / kAllWarps + unit - 1) / unit * unit;
+    lo = (int)min((long long)n, (long long)gw * per);
+    hi = (int)min((long long)n, (long long)lo + per);
+}
+
+// refs of the four pages from p on (a page past the end reads as in use).
+__device__ __forceinline__ int4 refs4(const int32_t *refs, int p, int end)
+{
+    if (p + 4 <= end)
+        return __ldcg(reinterpret_cast<const int4 *>(refs + p));
+    int4 r = make_int4(1, 1, 1, 1);
+    if (p < end)
+        r.x = __ldcg(refs + p);
+    if (p + 1 < end)
+        r.y = __ldcg(refs + p + 1);
+    if (p + 2 < end)
+        r.z = __ldcg(refs + p + 2);
+    return r;
+}
+
+__device__ __forceinline__ int count_free(const int4 &r) { return (r.x == 0) + (r.y == 0) + (r.z == 0) + (r.w == 0); }
+
+// Free pages of [lo, hi), which starts at a multiple of 4.
+__device__ int segment_free(const int32_t *refs, int lo, int hi, int lane)
+{
+    int n = 0;
+#pragma unroll 4
+    for (int p = lo + 4 * lane; p < hi; p += 128)
+        n += count_free(refs4(refs, p, hi));
+    return warp_sum(n);
+}
+
+// The ids of the free pages of [lo, hi), the first of which has rank `rank`, into
+// free_ids[rank], as far as ranks below `want` go.
+__device__ void write_free(const PoolParams &p, int lo, int hi, int rank, int want, int lane)
+{
+    for (int base = lo; base < hi && rank < want; base += 128) {
+        const int at = base + 4 * lane;
+        const int4 r = refs4(p.refs, at, hi);
+        const int n = count_free(r), before = warp_before(n, lane);
+        int k = rank + before;
+        if (r.x == 0 && k < want)
+            p.free_ids[k] = at;
+        k += r.x == 0;
+        if (r.y == 0 && k < want)
+            p.free_ids[k] = at + 1;
+        k += r.y == 0;
+        if (r.z == 0 && k < want)
+            p.free_ids[k] = at + 2;
+        k += r.z == 0;
+        if (r.w == 0 && k < want)
+            p.free_ids[k] = at + 3;
+        rank += __shfl_sync(0xffffffffu, before + n, 31);
+    }
+}
+
+// Collect every warp's counts in each CTA (behind a cluster barrier).
+__device__ void exchange(cg::cluster_group &cluster, Board &b)
+{
+    cluster.sync();
+    if (threadIdx.x < kAllWarps) {
+        const Board *from = cluster.map_shared_rank(&b, threadIdx.x / kWarps);
+        const int w = threadIdx.x % kWarps;
+        b.all_pages[threadIdx.x] = from->pages[w];
+        b.all_frees[threadIdx.x] = from->frees[w];
+        b.all_tokens[threadIdx.x] = from->tokens[w];
+    }
+    __syncthreads();
+}
+
+// Sum over the warps before gw, and over all, of one of the boards' arrays.
+template <typename T>
+__device__ __forceinline__ void before_and_total(const T *all, int gw, int lane, long long &before, long long &total)
+{
+    long long s = 0, t = 0;
+#pragma unroll
+    for (int k = 0; k < kAllWarps / 32; ++k) {
+        const long long v = all[32 * k + lane];
+        t += v;
+        s += 32 * k + lane < gw ? v : 0;
+    }
+    before = warp_sum64(s);
+    total = warp_sum64(t);
+}
+
+// Whether any CTA met an error (behind a cluster barrier; the caller passes another one
+// before it exits).
+__device__ bool any_error(cg::cluster_group &cluster, Board &b)
+{
+    int e = 0;
+    if (threadIdx.x < kCtas)
+        e = *cluster.map_shared_rank(&b.error, threadIdx.x);
+    return __syncthreads_or(e);
+}
+
+// Whether the entries in use of a row of `len` tokens are page ids, with refs when
+// `counted`; the lanes of a warp share the row.
+__device__ bool row_fine(const PoolParams &p, int row, int64_t len, bool counted, int lane)
+{
+    const int n = ceil_div(len, p.page_size);
+    bool ok = true;
+    for (int k = lane; k < n; k += 32) {
+        const int page = p.table[row * p.row_stride + k];
+        ok = ok && (unsigned)page < (unsigned)p.num_pages && (!counted || p.refs[page] > 0);
+    }
+    return __all_sync(0xffffffffu, ok);
+}
+
+__device__ __forceinline__ bool len_fine(const PoolParams &p, int64_t len)
+{
+    return len >= 0 && ceil_div(len, p.page_size) <= p.row_stride;
+}
+
+enum Op { kExtend, kFork };
+
+// kExtend: rows, add, slots. kFork: rows = children, add = parents, src, dst.
+template <Op OP>
+__global__ void __launch_bounds__(kThreads) grow_kernel(const PoolParams p, const int32_t *rows, const int32_t *add, int n,
+                                                        int64_t *slots, int64_t slots_capacity, int32_t *src,
+                                                        int32_t *dst)
+{
+    __shared__ Board b;
+    cg::cluster_group cluster = cg::this_cluster();
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, gw = (int)cluster.block_rank() * kWarps + warp;
+    const int P = p.page_size;
+    if (threadIdx.x == 0)
+        b.error = 0;
+    __syncthreads();
+    grid_dependency_wait();
+    grid_launch_dependents();
+
+    // What each entry of the warp's segment needs, and the free pages of its segment.
+    int e_lo, e_hi, p_lo, p_hi;
+    segment(n, 1, gw, e_lo, e_hi);
+    segment(p.num_pages, 4, gw, p_lo, p_hi);
+    auto need_of = [&](int i, long long &tokens) -> int {
+        tokens = 0;
+        if (i >= e_hi)
+            return 0;
+        const int row = rows[i];
+        if ((unsigned)row >= (unsigned)p.num_rows)
+            return -1;
+        const int64_t len = p.lens[row];
+        if (OP == kExtend) {
+            tokens = add[i];
+            if (tokens < 0 || !len_fine(p, len) || len + tokens > INT32_MAX || !len_fine(p, len + tokens)) {
+                tokens = 0;
+                return -1;
+            }
+            return ceil_div(len + tokens, P) - ceil_div(len, P);
+        }
+        const int parent = add[i];
+        if ((unsigned)parent >= (unsigned)p.num_rows || len != 0)
+            return -1;
+        const int64_t from = p.lens[parent];
+        return len_fine(p, from) ? from % P != 0 : -1;
+    };
+    long long pages = 0, tokens = 0;
+    for (int i0 = e_lo; i0 < e_hi; i0 += 32) {
+        const int i = i0 + lane;
+        long long t;
+        const int need = need_of(i, t);
+        if (need < 0)
+            b.error = 1;
+        else if (i < e_hi)
+            p.claim[rows[i]] = i;
+        pages += max(need, 0);
+        tokens += t;
+    }
+    pages = warp_sum64(pages);
+    tokens = warp_sum64(tokens);
+    if (pages > p.num_pages)  // more than there are: too many in any case
+        pages = p.num_pages + 1;
+    if (OP == kFork) {
+        for (int i = e_lo; i < e_hi; ++i) {
+            const int parent = add[i];
+            if ((unsigned)parent >= (unsigned)p.num_rows || !len_fine(p, p.lens[parent]) ||
+                !row_fine(p, parent, p.lens[parent], true, lane))
+                b.error = 1;
+        }
+    }
+    const int frees = segment_free(p.refs, p_lo, p_hi, lane);
+    if (lane == 0) {
+        b.pages[warp] = (int32_t)pages;
+        b.frees[warp] = frees;
+        b.tokens[warp] = tokens;
+    }
+    exchange(cluster, b);
+
+    // Ranks: an entry's first new page and slot, the ids of the free pages that are wanted.
+    long long page_at, want, rank, there, token_at, all_tokens;
+    before_and_total(b.all_pages, gw, lane, page_at, want);
+    before_and_total(b.all_frees, gw, lane, rank, there);
+    before_and_total(b.all_tokens, gw, lane, token_at, all_tokens);
+    const bool too_many = want > there;
+    const bool no_room = OP == kExtend && slots && all_tokens > slots_capacity;
+    if (!too_many)
+        write_free(p, p_lo, p_hi, (int)rank, (int)want, lane);
+    for (int i0 = e_lo; i0 < e_hi; i0 += 32) {
+        const int i = i0 + lane;
+        long long t;
+        const int need = max(need_of(i, t), 0);
+        const int before = warp_before(need, lane);
+        const long long t_before = warp_before64(t, lane);
+        if (i < e_hi) {
+            p.first[i] = (int32_t)(page_at + before);
+            const int row = rows[i], parent = OP == kFork ? add[i] : 0;
+            if (OP == kExtend)
+                p.first_slot[i] = token_at + t_before;
+            else if ((unsigned)parent < (unsigned)p.num_rows)
+                p.first_slot[i] = p.lens[parent];
+            if ((unsigned)row < (unsigned)p.num_rows && __ldcg(p.claim + row) != i)
+                b.error = 1;  // another entry names the row too
+        }
+        page_at += __shfl_sync(0xffffffffu, before + need, 31);
+        token_at += __shfl_sync(0xffffffffu, t_before + t, 31);
+    }
+    cluster.sync();
+
+    const bool bad = any_error(cluster, b);
+    if (bad || too_many || no_room) {
+        // nothing changes; the outputs say "no page", which the calls that take them skip
+        if (gw == 0 && lane == 0)
+            record_status(p.status, bad || no_room ? PKV_ERR_DEVICE_BOUNDS : PKV_ERR_OOM);
+        const int64_t at = (int64_t)gw * 32 + lane;
+        if (OP == kFork)
+            for (int64_t i = at; i < n; i += kAllWarps * 32)
+                src[i] = dst[i] = -1;
+        else if (slots)
+            for (int64_t i = at; i < slots_capacity; i += kAllWarps * 32)
+                slots[i] = -1;
+    } else if (OP == kExtend) {
+        for (int i = gw; i < n; i += kAllWarps) {
+            const int row = rows[i], len = p.lens[row], more = add[i];
+            const int have = ceil_div(len, P), upto = ceil_div((int64_t)len + more, P);
+            int32_t *entries = p.table + row * p.row_stride;
+            const int32_t *fresh = p.free_ids + __ldcg(p.first + i);
+            for (int k = have + lane; k < upto; k += 32) {
+                const int page = __ldcg(fresh + k - have);
+                entries[k] = page;
+                p.refs[page] = 1;
+            }
+            if (slots) {
+                int64_t *out = slots + __ldcg(p.first_slot + i);
+                const int last = have > 0 ? entries[have - 1] : 0;  // filled up first
+                for (int t = lane; t < more; t += 32) {
+                    const int at = len + t, k = (unsigned)at / (unsigned)P;
+                    const int page = k < have ? last : __ldcg(fresh + k - have);
+                    out[t] = (int64_t)page * P + (at - k * P);
+                }
+            }
+            __syncwarp();  // every lane has the row's old length
+            if (lane == 0)
+                p.lens[row] = len + more;
+        }
+    } else {
+        for (int i = gw; i < n; i += kAllWarps) {
+            const int child = rows[i], parent = add[i], len = (int)__ldcg(p.first_slot + i);
+            const int full = len / P;
+            const int32_t *from = p.table + parent * p.row_stride;
+            int32_t *to = p.table + child * p.row_stride;
+            for (int k = lane; k < full; k += 32) {
+                const int page = from[k];
+                to[k] = page;
+                atomicAdd(p.refs + page, 1);
+            }
+            if (lane == 0) {
+                int a = -1, z = -1;
+                if (len % P != 0) {
+                    a = from[full];
+                    z = __ldcg(p.free_ids + __ldcg(p.first + i));
+                    to[full] = z;
+                    p.refs[z] = 1;
+                }
+                src[i] = a;
+                dst[i] = z;
+                p.lens[child] = len;
+            }
+        }
+    }
+    cluster.sync();  // no CTA leaves while another reads its board
+}
+
+__global__ void __launch_bounds__(kThreads) free_kernel(const PoolParams p, const int32_t *rows, int n)
+{
+    __shared__ Board b;
+    cg::cluster_group cluster = cg::this_cluster();
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, gw = (int)cluster.block_rank() * kWarps + warp;
+    if (threadIdx.x == 0)
+        b.error = 0;
+    __syncthreads();
+    grid_dependency_wait();
+    grid_launch_dependents();
+    for (int i = gw; i < n; i += kAllWarps) {
+        const int row = rows[i];
+        if ((unsigned)row >= (unsigned)p.num_rows || !len_fine(p, p.lens[row]) ||
+            !row_fine(p, row, p.lens[row], true, lane))
+            b.error = 1;
+        else if (lane == 0)
+            p.claim[row] = i;
+    }
+    cluster.sync();
+    for (int i = gw * 32 + lane; i < n; i += kAllWarps * 32)
+        if ((unsigned)rows[i] < (unsigned)p.num_rows && __ldcg(p.claim + rows[i]) != i)
+            b.error = 1;
+    cluster.sync();
+    if (any_error(cluster, b)) {
+        if (gw == 0 && lane == 0)
+            record_status(p.status, PKV_ERR_DEVICE_BOUNDS);
+    } else {
+        for (int i = gw; i < n; i += kAllWarps) {
+            const int row = rows[i], pages = ceil_div(p.lens[row], p.page_size);
+            for (int k = lane; k < pages; k += 32) {
+                int32_t *r = p.refs + p.table[row * p.row_stride + k];
+                if (atomicSub(r, 1) <= 0) {  // more entries named the page than were counted
+                    atomicAdd(r, 1);
+                    record_status(p.status, PKV_ERR_DEVICE_BOUNDS);
+                }
+            }
+            __syncwarp();
+            if (lane == 0)
+                p.lens[row] = 0;
+        }
+    }
+    cluster.sync();
+}
+
+// The moves of a compaction: src, dst, their number, refs_out, and in the workspace each
+// moved page's rank and the number of live pages.
+__global__ void __launch_bounds__(kThreads) moves_kernel(const PoolParams p, int32_t *refs_out, int32_t *src,
+                                                         int32_t *dst, int max_moves, int32_t *count)
+{
+    __shared__ Board b;
+    __shared__ int edge_live;  // live pages below n_live in the segment that n_live falls into
+    cg::cluster_group cluster = cg::this_cluster();
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, gw = (int)cluster.block_rank() * kWarps + warp;
+    grid_dependency_wait();
+    grid_launch_dependents();
+    int lo, hi;
+    segment(p.num_pages, 4, gw, lo, hi);
+    const int frees = segment_free(p.refs, lo, hi, lane);
+    if (lane == 0) {
+        b.pages[warp] = hi - lo - frees;  // live
+        b.frees[warp] = frees;
+        b.tokens[warp] = 0;
+    }
+    exchange(cluster, b);
+    long long live_before, n_live, free_before, n_free;
+    before_and_total(b.all_pages, gw, lane, live_before, n_live);
+    before_and_total(b.all_frees, gw, lane, free_before, n_free);
+    // The holes are the free pages below n_live: a warp's first has rank free_before. The
+    // movers are the live pages from n_live on: rank = live pages before it minus those
+    // below n_live, n_live - holes.
+    const int N = (int)n_live;
+    const int per = ((p.num_pages + kAllWarps - 1) / kAllWarps + 3) / 4 * 4;
+    const int edge = min(N / max(per, 1), kAllWarps - 1);
+    if (warp == 0) {
+        int e_lo, e_hi;
+        segment(p.num_pages, 4, edge, e_lo, e_hi);
+        int n = 0;
+        for (int q = e_lo + lane; q < min(e_hi, N); q += 32)
+            n += __ldcg(p.refs + q) != 0;
+        n = warp_sum(n);
+        if (lane == 0)
+            edge_live = n;
+    }
+    __syncthreads();
+    long long edge_before, unused;
+    before_and_total(b.all_pages, edge, lane, edge_before, unused);
+    const int live_below = (int)edge_before + edge_live;
+    const int moves = N - live_below;  // as many movers as holes
+    const bool fits = moves <= max_moves;
+    if (fits) {
+        int live_rank = (int)live_before - live_below, free_rank = (int)free_before;
+        for (int base = lo; base < hi; base += 128) {
+            const int at = base + 4 * lane;
+            const int4 r4 = refs4(p.refs, at, hi);
+            const int r[4] = {r4.x, r4.y, r4.z, r4.w};
+            int f = 0, l = 0;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                f += at + k < hi && r[k] == 0;
+                l += at + k < hi && r[k] != 0;
+            }
+            const int f_before = warp_before(f, lane), l_before = warp_before(l, lane);
+            int fr = free_rank + f_before, lr = live_rank + l_before;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int q = at + k;
+                if (q >= hi)
+                    break;
+                if (r[k] == 0) {
+                    if (q < N)
+                        dst[fr] = q;
+                    else
+                        p.free_ids[q] = -1;
+                    ++fr;
+                } else {
+                    if (q >= N) {
+                        src[lr] = q;
+                        p.free_ids[q] = lr;
+                    }
+                    ++lr;
+                }
+            }
+            free_rank += __shfl_sync(0xffffffffu, f_before + f, 31);
+            live_rank += __shfl_sync(0xffffffffu, l_before + l, 31);
+        }
+    }
+    cluster.sync();
+    const int at = gw * 32 + lane;
+    if (fits) {
+        if (refs_out != p.refs)  // what stays, and the ids that are given up
+            for (int q = at; q < p.num_pages; q += kAllWarps * 32) {
+                const int r = __ldcg(p.refs + q);
+                if (q >= N)
+                    refs_out[q] = 0;
+                else if (r != 0)
+                    refs_out[q] = r;
+            }
+        for (int k = at; k < moves; k += kAllWarps * 32) {
+            const int from = __ldcg(src + k);
+            refs_out[__ldcg(dst + k)] = __ldcg(p.refs + from);
+            if (refs_out == p.refs)
+                refs_out[from] = 0;
+        }
+    } else if (refs_out != p.refs) {
+        for (int q = at; q < p.num_pages; q += kAllWarps * 32)
+            refs_out[q] = __ldcg(p.refs + q);
+    }
+    if (at == 0) {
+        *count = fits ? moves : 0;
+        *p.word = fits ? N : INT32_MAX;  // ids below it stay what they are
+        if (!fits)
+            record_status(p.status, PKV_ERR_DEVICE_BOUNDS);
+    }
+    cluster.sync();
+}
+
+// Table entries by the moves: one warp a row.
+__global__ void __launch_bounds__(256) rewrite_kernel(const PoolParams p, int32_t *table_out, int64_t out_stride,
+                                                      int32_t *lens_out, const int32_t *dst)
+{
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int lane = threadIdx.x % 32;
+    const int row = blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32;
+    if (row >= p.num_rows)
+        return;
+    const int n_live = *p.word;
+    const int64_t len = p.lens[row];
+    if (!len_fine(p, len)) {
+        if (lane == 0)
+            record_status(p.status, PKV_ERR_DEVICE_BOUNDS);
+        return;
+    }
+    const int n = ceil_div(len, p.page_size);
+    const int32_t *from = p.table + row * p.row_stride;
+    int32_t *to = table_out + row * out_stride;
+    for (int k = lane; k < n; k += 32) {
+        int page = from[k];
+        if ((unsigned)page >= (unsigned)p.num_pages) {
+            record_status(p.status, PKV_ERR_DEVICE_BOUNDS);
+        } else if (page >= n_live) {
+            const int rank = p.free_ids[page];
+            if (rank >= 0)
+                page = dst[rank];
+            else
+                record_status(p.status, PKV_ERR_DEVICE_BOUNDS);  // an entry that refs did not count
+        }
+        to[k] = page;
+    }
+    if (lane == 0 && lens_out != p.lens)
+        lens_out[row] = (int32_t)len;
+}
+
+// Whole pages of K and V, of every layer, in 16-byte granules: a CTA takes tiles of
+// kTile granules of one cache, each thread kUnroll of them, all loaded before the first
+// is stored. Bound by HBM.
+constexpr int kCopyThreads = 256, kUnroll = 8, kTile = kCopyThreads * kUnroll;
+
+struct CopyParams {
+    uint8_t *k, *v;
+    int64_t layer_bytes;  // from one layer's cache to the next
+    int32_t num_layers, num_pages;
+    int32_t granules;     // of a page
+    int32_t n;
+    const int32_t *src, *dst, *count;
+    int32_t *status;
+};
+
+__global__ void __launch_bounds__(kCopyThreads) copy_kernel(const CopyParams p)
+{
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int n = p.count ? max(0, min(p.n, *p.count)) : p.n;
+    const long long per_cache = ((long long)n * p.granules + kTile - 1) / kTile;
+    for (long long tile = blockIdx.x; tile < per_cache * 2 * p.num_layers; tile += gridDim.x) {
+        const long long which = tile / per_cache;
+        uint8_t *cache = (which & 1 ? p.v : p.k) + (which >> 1) * p.layer_bytes;
+        const long long g0 = (tile - which * per_cache) * kTile;
+        const int pair0 = (int)(g0 / p.granules), rest = (int)(g0 - (long long)pair0 * p.granules);
+        uint4 x[kUnroll];
+        int64_t to[kUnroll];
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            const unsigned g = (unsigned)rest + u * kCopyThreads + threadIdx.x;
+            const int step = g / (unsigned)p.granules;
+            const int pair = pair0 + step;
+            to[u] = -1;
+            if (pair < n) {
+                const int a = __ldg(p.src + pair), z = __ldg(p.dst + pair);
+                if (a >= p.num_pages || z >= p.num_pages) {
+                    if (p.status)
+                        record_status(p.status, PKV_ERR_DEVICE_BOUNDS);
+                } else if (a >= 0 && z >= 0) {
+                    const int64_t in = (int64_t)(g - (unsigned)step * (unsigned)p.granules) * 16;
+                    const int64_t page = (int64_t)p.granules * 16;
+                    x[u] = *reinterpret_cast<const uint4 *>(cache + a * page + in);
+                    to[u] = z * page + in;
+                }
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u)
+            if (to[u] >= 0)
+                *reinterpret_cast<uint4 *>(cache + to[u]) = x[u];
+    }
+}
+
+int refuse(int status, const char *call, const char *what)
+{
+    set_last_error((std::string(call) + ": " + what).c_str());
+    return status;
+}
+
+bool misaligned(const void *p, uintptr_t a) { return (uintptr_t)p % a != 0; }
+
+int64_t align256(int64_t x) { return (x + 255) / 256 * 256; }
+
+struct Carve {
+    int64_t claim, first, first_slot, free_ids, word, bytes;
+};
+
+Carve carve(int32_t num_rows, int32_t num_pages)
+{
+    Carve c{};
+    c.claim = 0;
+    c.first = align256(c.claim + 4LL * num_rows);
+    c.first_slot = align256(c.first + 4LL * num_rows);
+    c.free_ids = align256(c.first_slot + 8LL * num_rows);
+    c.word = align256(c.free_ids + 4LL * num_pages);
+    c.bytes = c.word + 256;
+    return c;
+}
+
+// The pool's checks, and its parameters.
+int take_pool(const char *call, const pkv_page_pool *pool, PoolParams &p)
+{
+    if (!pool)
+        return refuse(PKV_ERR_INVALID_ARG, call, "pool is NULL");
+    if (pool->num_rows < 0 || pool->num_pages < 0 || pool->row_stride < 0 || pool->page_size <= 0)
+        return refuse(PKV_ERR_INVALID_ARG, call, "negative size, or page_size <= 0");
+    if (pool->row_stride > INT32_MAX || pool->num_pages > INT32_MAX - 4096)
+        return refuse(PKV_ERR_UNSUPPORTED, call, "a row or a pool of about 2^31 pages or more");
+    if ((pool->num_rows > 0 && (!pool->lens || (pool->row_stride > 0 && !pool->table))) ||
+        (pool->num_pages > 0 && !pool->refs) || !pool->status)
+        return refuse(PKV_ERR_INVALID_ARG, call, "table, lens, refs and status are required");
+    if (misaligned(pool->table, 4) || misaligned(pool->lens, 4) || misaligned(pool->refs, 16) ||
+        misaligned(pool->status, 4) || misaligned(pool->workspace, 16))
+        return refuse(PKV_ERR_INVALID_ARG, call, "refs and workspace must be 16-byte aligned, the others 4-byte");
+    const Carve c = carve(pool->num_rows, pool->num_pages);
+    if (!pool->workspace || pool->workspace_bytes < c.bytes)
+        return refuse(PKV_ERR_INVALID_ARG, call, "workspace is NULL or below pkv_pages_workspace's size");
+    uint8_t *w = (uint8_t *)pool->workspace;
+    p = PoolParams{};
+    p.table = pool->table;
+    p.lens = pool->lens;
+    p.refs = pool->refs;
+    p.row_stride = pool->row_stride;
+    p.num_rows = pool->num_rows;
+    p.num_pages = pool->num_pages;
+    p.page_size = pool->page_size;
+    p.status = pool->status;
+    p.claim = (int32_t *)(w + c.claim);
+    p.first = (int32_t *)(w + c.first);
+    p.first_slot = (int64_t *)(w + c.first_slot);
+    p.free_ids = (int32_t *)(w + c.free_ids);
+    p.word = (int32_t *)(w + c.word);
+    return PKV_OK;
+}
+
+int take_entries(const char *call, const PoolParams &p, int32_t n, const void *a, const void *b)
+{
+    if (n < 0)
+        return refuse(PKV_ERR_INVALID_ARG, call, "n is negative");
+    if (n > p.num_rows)
+        return refuse(PKV_ERR_INVALID_ARG, call, "more entries than the pool has rows");
+    if (n > 0 && (!a || !b || misaligned(a, 4) || misaligned(b, 4)))
+        return refuse(PKV_ERR_INVALID_ARG, call, "an index array is NULL or misaligned");
+    return PKV_OK;
+}
+
+// One launch behind the work of the stream, its start allowed to overlap the end of the
+// kernel before it (which every kernel here waits for first thing).
+template <typename... Params, typename... Args>
+cudaError_t launch(void (*kernel)(Params...), int grid, int threads, int cluster, void *stream, Args... args)
+{
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.stream = (cudaStream_t)stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+int launched(const char *call, cudaError_t ce)
+{
+    return ce == cudaSuccess ? PKV_OK : refuse(PKV_ERR_CUDA, call, cudaGetErrorString(ce));
+}
+
+}  // namespace
+}  // namespace pkv
+
+extern "C" {
+
+PKV_API int pkv_pages_workspace(int32_t num_rows, int32_t num_pages, int64_t *bytes)
+{
+    using namespace pkv;
+    if (!bytes || num_rows < 0 || num_pages < 0)
+        return refuse(PKV_ERR_INVALID_ARG, "pkv_pages_workspace", "bytes is NULL or a size negative");
+    *bytes = carve(num_rows, num_pages).bytes;
+    return PKV_OK;
+}
+
+PKV_API int pkv_pages_extend(const pkv_page_pool *pool, const int32_t *rows, const int32_t *add, int32_t n,
+                             int64_t *slots, int64_t slots_capacity, void *stream)
+{
+    using namespace pkv;
+    NvtxRange range("pkv_pages_extend");
+    set_last_error("");
+    PoolParams p;
+    int st = take_pool("pkv_pages_extend", pool, p);
+    if (st == PKV_OK)
+        st = take_entries("pkv_pages_extend", p, n, rows, add);
+    if (st != PKV_OK)
+        return st;
+    if (slots_capacity < 0 || misaligned(slots, 8))
+        return refuse(PKV_ERR_INVALID_ARG, "pkv_pages_extend", "slots are misaligned or their capacity negative");
+    if (n == 0)
+        return PKV_OK;
+    return launched("pkv_pages_extend", launch(grow_kernel<kExtend>, kCtas, kThreads, kCtas, stream, p, rows, add, n,
+                                               slots, slots_capacity, (int32_t *)nullptr, (int32_t *)nullptr));
+}
+
+PKV_API int pkv_pages_fork(const pkv_page_pool *pool, const int32_t *parents, const int32_t *children, int32_t n,
+                           int32_t *src, int32_t *dst, void *stream)
+{
+    using namespace pkv;
+    NvtxRange range("pkv_pages_fork");
+    set_last_error("");
+    PoolParams p;
+    int st = take_pool("pkv_pages_fork", pool, p);
+    if (st == PKV_OK)
+        st = take_entries("pkv_pages_fork", p, n, parents, children);
+    if (st == PKV_OK)
+        st = take_entries("pkv_pages_fork", p, n, src, dst);
+    if (st != PKV_OK || n == 0)
+        return st;
+    return launched("pkv_pages_fork", launch(grow_kernel<kFork>, kCtas, kThreads, kCtas, stream, p, children, parents, n,
+                                             (int64_t *)nullptr, (int64_t)0, src, dst));
+}
+
+PKV_API int pkv_pages_free(const pkv_page_pool *pool, const int32_t *rows, int32_t n, void *stream)
+{
+    using namespace pkv;
+    NvtxRange range("pkv_pages_free");
+    set_last_error("");
+    PoolParams p;
+    int st = take_pool("pkv_pages_free", pool, p);
+    if (st == PKV_OK)
+        st = take_entries("pkv_pages_free", p, n, rows, rows);
+    if (st != PKV_OK || n == 0)
+        return st;
+    return launched("pkv_pages_free", launch(free_kernel, kCtas, kThreads, kCtas, stream, p, rows, n));
+}
+
+PKV_API int pkv_pages_compact(const pkv_page_pool *pool, const pkv_page_pool *out, int32_t *src, int32_t *dst,
+                              int32_t max_moves, int32_t *count, void *stream)
+{
+    using namespace pkv;
+    NvtxRange range("pkv_pages_compact");
+    set_last_error("");
+    PoolParams p, o;
+    int st = take_pool("pkv_pages_compact", pool, p);
+    if (st == PKV_OK)
+        st = take_pool("pkv_pages_compact", out, o);
+    if (st != PKV_OK)
+        return st;
+    if (o.num_rows != p.num_rows || o.num_pages != p.num_pages || o.page_size != p.page_size ||
+        o.row_stride < p.row_stride)
+        return refuse(PKV_ERR_INVALID_ARG, "pkv_pages_compact", "the two pools differ in their sizes");
+    if (o.table == p.table && o.row_stride != p.row_stride)
+        return refuse(PKV_ERR_INVALID_ARG, "pkv_pages_compact", "one table with two row strides");
+    if (max_moves < 0 || (max_moves > 0 && (!src || !dst)) || !count || misaligned(src, 4) || misaligned(dst, 4) ||
+        misaligned(count, 4))
+        return refuse(PKV_ERR_INVALID_ARG, "pkv_pages_compact", "src, dst and count are required");
+    cudaError_t ce = launch(moves_kernel, kCtas, kThreads, kCtas, stream, p, o.refs, src, dst, (int)max_moves, count);
+    if (ce == cudaSuccess && p.num_rows > 0)
+        ce = launch(rewrite_kernel, (p.num_rows + 7) / 8, 256, 1, stream, p, o.table, o.row_stride, o.lens,
+                    (const int32_t *)dst);
+    return launched("pkv_pages_compact", ce);
+}
+
+PKV_API int pkv_copy_pages(void *k_cache, void *v_cache, int32_t num_layers, int64_t layer_bytes, int32_t num_pages,
+                           int64_t page_bytes, const int32_t *src, const int32_t *dst, int32_t n, const int32_t *count,
+                           int32_t *status, void *stream)
+{
+    using namespace pkv;
+    NvtxRange range("pkv_copy_pages");
+    set_last_error("");
+    if (n < 0 || num_layers < 0 || num_pages < 0 || page_bytes < 0 || layer_bytes < 0)
+        return refuse(PKV_ERR_INVALID_ARG, "pkv_copy_pages", "negative size");
+    if (page_bytes % 16 || layer_bytes % 16 || page_bytes > (1LL << 30))
+        return refuse(PKV_ERR_UNSUPPORTED, "pkv_copy_pages",
+                      "page_bytes and layer_bytes must be multiples of 16, a page at most 2^30 bytes");
+    if (n == 0 || num_layers == 0 || page_bytes == 0)
+        return PKV_OK;
+    if (!k_cache || !v_cache || !src || !dst)
+        return refuse(PKV_ERR_INVALID_ARG, "pkv_copy_pages", "a required pointer is NULL");
+    if (misaligned(k_cache, 16) || misaligned(v_cache, 16) || misaligned(src, 4) || misaligned(dst, 4) ||
+        misaligned(count, 4) || misaligned(status, 4))
+        return refuse(PKV_ERR_INVALID_ARG, "pkv_copy_pages", "caches must be 16-byte aligned, the others 4-byte");
+    CopyParams p{};
+    p.k = (uint8_t *)k_cache;
+    p.v = (uint8_t *)v_cache;
+    p.layer_bytes = layer_bytes;
+    p.num_layers = num_layers;
+    p.num_pages = num_pages;
+    p.granules = (int32_t)(page_bytes / 16);
+    p.n = n;
+    p.src = src;
+    p.dst = dst;
+    p.count = count;
+    p.status = status;
+    int dev = 0, sms = 148;
+    if (cudaGetDevice(&dev) == cudaSuccess)
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    const int64_t tiles = ((int64_t)n * p.granules + kTile - 1) / kTile * 2 * num_layers;
+    const int grid = (int)(tiles < sms * 8LL ? tiles : sms * 8LL);
+    return launched("pkv_copy_pages", launch(copy_kernel, grid, kCopyThreads, 1, stream, p));
+}
+
+}  // extern "C"

@@ -44,7 +44,9 @@ EXPORTED = ("pkv_plan_create", "pkv_run", "pkv_merge_state", "pkv_plan_destroy",
             "pkv_plan_get_info", "pkv_plan_device_status", "pkv_status_string",
             "pkv_last_error", "pkv_abi_version", "pkv_plan_set_timing_events",
             "pkv_decode_noalloc", "pkv_plan_create_capturable", "pkv_plan_update",
-            "pkv_build_kv_indices", "pkv_plan_create_sinks", "pkv_norm_rope_append")
+            "pkv_build_kv_indices", "pkv_plan_create_sinks", "pkv_norm_rope_append",
+            "pkv_pages_workspace", "pkv_pages_extend", "pkv_pages_fork", "pkv_pages_free",
+            "pkv_pages_compact", "pkv_copy_pages")
 
 
 class PkvError(RuntimeError):
@@ -113,6 +115,22 @@ class AppendDesc(ctypes.Structure):
     ]
 
 
+class PoolDesc(ctypes.Structure):
+    _fields_ = [
+        ("table", ctypes.c_void_p),
+        ("lens", ctypes.c_void_p),
+        ("refs", ctypes.c_void_p),
+        ("row_stride", ctypes.c_int64),
+        ("num_rows", ctypes.c_int32),
+        ("num_pages", ctypes.c_int32),
+        ("page_size", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+        ("workspace", ctypes.c_void_p),
+        ("workspace_bytes", ctypes.c_int64),
+        ("status", ctypes.c_void_p),
+    ]
+
+
 class PlanInfo(ctypes.Structure):
     _fields_ = [
         ("kind", ctypes.c_int32),
@@ -175,6 +193,15 @@ def load_library(path: Optional[str] = None):
         lib.pkv_build_kv_indices.restype = ctypes.c_int
         lib.pkv_norm_rope_append.argtypes = [ctypes.POINTER(AppendDesc)] + [vp] * 14
         lib.pkv_norm_rope_append.restype = ctypes.c_int
+        pool = ctypes.POINTER(PoolDesc)
+        for name, args in (("pkv_pages_workspace", [i32, i32, ctypes.POINTER(i64)]),
+                           ("pkv_pages_extend", [pool, vp, vp, i32, vp, i64, vp]),
+                           ("pkv_pages_fork", [pool, vp, vp, i32, vp, vp, vp]),
+                           ("pkv_pages_free", [pool, vp, i32, vp]),
+                           ("pkv_pages_compact", [pool, pool, vp, vp, i32, vp, vp]),
+                           ("pkv_copy_pages", [vp, vp, i32, i64, i32, i64, vp, vp, i32, vp, vp, vp])):
+            getattr(lib, name).argtypes = args
+            getattr(lib, name).restype = ctypes.c_int
         lib.pkv_abi_version.argtypes = []
         lib.pkv_abi_version.restype = ctypes.c_int
         _lib = lib
@@ -188,10 +215,26 @@ def _check(status: int, what: str):
         raise PkvError(status, f"{what}: {msg}")
 
 
+# The current stream's handle without a Stream object around it (a third of the host time
+# of a small call), where this torch has it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream_handle(stream=None) -> int:
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         stream = torch.cuda.current_stream()
     return int(stream.cuda_stream)
+
+
+def _ptrs(*tensors):
+    return [None if t is None else t.data_ptr() for t in tensors]
+
+
+def _sig(t):
+    """What a call's checks and its descriptor go by: a tensor's type, shape, strides and device."""
+    return None if t is None else (t.dtype, t.shape, t.stride(), t.device)
 
 
 def _host_i32(a):
@@ -406,33 +449,20 @@ def _want(t: Optional[torch.Tensor], name: str, dtype, shape=None):
         raise ValueError(f"{name} must be a contiguous CUDA {dtype} tensor" + (f" of shape {tuple(shape)}" if shape else ""))
 
 
-def _here(*tensors):
+def _here(dev: int, *tensors):
     """The tensors live on the current device, whose stream the call is launched on."""
-    dev = torch.cuda.current_device()
     for t in tensors:
         if t is not None and t.device.index != dev:
             raise ValueError(f"a tensor on {t.device}, but the current device is cuda:{dev}")
 
 
-def norm_rope_append(q: Optional[torch.Tensor], k: Optional[torch.Tensor], v: Optional[torch.Tensor] = None, *,
-                     positions: Optional[torch.Tensor] = None, cos_sin: Optional[torch.Tensor] = None,
-                     slots: Optional[torch.Tensor] = None, k_cache: Optional[torch.Tensor] = None,
-                     v_cache: Optional[torch.Tensor] = None, q_weight: Optional[torch.Tensor] = None,
-                     k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6, weight_offset: float = 0.0,
-                     interleaved: bool = False, k_scale: float = 1.0, v_scale: float = 1.0,
-                     q_out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None,
-                     status: Optional[torch.Tensor] = None, stream=None):
-    """Normalise each head of q and k, rotate them by their tokens' positions and write k
-    and v into the paged caches, in one pass; returns q_out (None without q).
+# Checked descriptors of earlier calls by what they were made from (types, shapes, strides
+# and scalars), which a layer's calls of one step share.
+_append_descs: dict = {}
 
-    q [n, H_qo, d], k and v [n, H_kv, d] bf16, possibly slices of one projection (heads
-    contiguous, any token stride); q_weight / k_weight [d] bf16 (None: no norm); cos_sin
-    [max_position, rotary_dim] fp32 (cosines, then sines; None: no rotation); positions
-    [n] int32; slots [n] int64 (page * page_size + offset; negative: a padding row, not
-    written); caches [num_pages, P, H_kv, d] bf16, float8_e4m3fn or float8_e5m2, or both
-    None with k_out [n, H_kv, d]. status: device int32 word for out-of-range slots and
-    positions."""
-    lib = _lib or load_library()
+
+def _append_desc(dev, eps, weight_offset, interleaved, k_scale, v_scale, q, k, v, q_weight, k_weight, cos_sin, positions,
+                 slots, q_out, k_out, k_cache, v_cache, status):
     d = AppendDesc()
     n = dim = None
     for t, name in ((q, "q"), (k, "k"), (v, "v")):
@@ -471,20 +501,170 @@ def norm_rope_append(q: Optional[torch.Tensor], k: Optional[torch.Tensor], v: Op
         _want(k_cache, "k_cache", k_cache.dtype)
         _want(v_cache, "v_cache", k_cache.dtype, k_cache.shape)
         d.num_pages, d.page_size, d.kv_dtype = k_cache.shape[0], k_cache.shape[1], code
-    if q is not None and q_out is None:
-        q_out = torch.empty((n, d.num_qo_heads, dim), dtype=torch.bfloat16, device=q.device)
     if q is not None:
         _want(q_out, "q_out", torch.bfloat16, (n, d.num_qo_heads, dim))
     if k is not None:
         _want(k_out, "k_out", torch.bfloat16, (n, d.num_kv_heads, dim))
-    _here(q, k, v, positions, cos_sin, slots, k_cache, v_cache, q_weight, k_weight, q_out, k_out, status)
+    _here(dev, q, k, v, positions, cos_sin, slots, k_cache, v_cache, q_weight, k_weight, q_out, k_out, status)
     d.eps, d.weight_offset, d.interleaved = eps, weight_offset, 1 if interleaved else 0
     d.k_scale, d.v_scale = k_scale, v_scale
-    _check(lib.pkv_norm_rope_append(ctypes.byref(d), _ptr(q), _ptr(k), _ptr(v), _ptr(q_weight), _ptr(k_weight),
-                                    _ptr(cos_sin), _ptr(positions), _ptr(slots), _ptr(q_out), _ptr(k_out),
-                                    _ptr(k_cache), _ptr(v_cache), _ptr(status), _stream_handle(stream)),
-           "pkv_norm_rope_append")
+    return d
+
+
+def norm_rope_append(q: Optional[torch.Tensor], k: Optional[torch.Tensor], v: Optional[torch.Tensor] = None, *,
+                     positions: Optional[torch.Tensor] = None, cos_sin: Optional[torch.Tensor] = None,
+                     slots: Optional[torch.Tensor] = None, k_cache: Optional[torch.Tensor] = None,
+                     v_cache: Optional[torch.Tensor] = None, q_weight: Optional[torch.Tensor] = None,
+                     k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6, weight_offset: float = 0.0,
+                     interleaved: bool = False, k_scale: float = 1.0, v_scale: float = 1.0,
+                     q_out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None,
+                     status: Optional[torch.Tensor] = None, stream=None):
+    """Normalise each head of q and k, rotate them by their tokens' positions and write k
+    and v into the paged caches, in one pass; returns q_out (None without q).
+
+    q [n, H_qo, d], k and v [n, H_kv, d] bf16, possibly slices of one projection (heads
+    contiguous, any token stride); q_weight / k_weight [d] bf16 (None: no norm); cos_sin
+    [max_position, rotary_dim] fp32 (cosines, then sines; None: no rotation); positions
+    [n] int32; slots [n] int64 (page * page_size + offset; negative: a padding row, not
+    written); caches [num_pages, P, H_kv, d] bf16, float8_e4m3fn or float8_e5m2, or both
+    None with k_out [n, H_kv, d]. status: device int32 word for out-of-range slots and
+    positions."""
+    lib = _lib or load_library()
+    if q is not None and q_out is None:
+        q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+    dev = torch.cuda.current_device()
+    tensors = (q, k, v, q_weight, k_weight, cos_sin, positions, slots, q_out, k_out, k_cache, v_cache, status)
+    key = (dev, eps, weight_offset, interleaved, k_scale, v_scale) + tuple(map(_sig, tensors))
+    d = _append_descs.get(key)
+    if d is None:
+        d = _append_desc(dev, eps, weight_offset, interleaved, k_scale, v_scale, *tensors)
+        if len(_append_descs) >= 1024:
+            _append_descs.clear()
+        _append_descs[key] = d
+    _check(lib.pkv_norm_rope_append(d, *_ptrs(*tensors), _stream_handle(stream)), "pkv_norm_rope_append")
     return q_out
+
+
+class PagePool:
+    """The pages of a cache on the device: table [rows, max_pages] page ids, lens [rows]
+    tokens and refs [num_pages] int32 (how many table entries in use name a page; 0: free),
+    all CUDA tensors that stay the caller's. Calls are asynchronous on the current stream;
+    what they could not do is in device_status(). A pool's calls share its workspace, so
+    they must not overlap on several streams."""
+
+    def __init__(self, table: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor, *, page_size: int):
+        self._lib = load_library()
+        if table.dim() != 2 or lens.dim() != 1 or refs.dim() != 1 or lens.shape[0] != table.shape[0]:
+            raise ValueError("table is [rows, max_pages], lens [rows], refs [num_pages]")
+        for t, name in ((table, "table"), (lens, "lens"), (refs, "refs")):
+            _want(t, name, torch.int32)
+        _here(torch.cuda.current_device(), table, lens, refs)
+        self.table, self.lens, self.refs, self.page_size = table, lens, refs, int(page_size)
+        size = ctypes.c_int64()
+        _check(self._lib.pkv_pages_workspace(table.shape[0], refs.shape[0], ctypes.byref(size)), "pkv_pages_workspace")
+        self._workspace = torch.empty(size.value, dtype=torch.uint8, device=table.device)
+        self._status = torch.zeros(1, dtype=torch.int32, device=table.device)
+        d = PoolDesc()
+        d.table, d.lens, d.refs = table.data_ptr(), lens.data_ptr(), refs.data_ptr()
+        d.row_stride, d.num_rows, d.num_pages, d.page_size = table.shape[1], table.shape[0], refs.shape[0], self.page_size
+        d.workspace, d.workspace_bytes, d.status = self._workspace.data_ptr(), size.value, self._status.data_ptr()
+        self._desc = d
+
+    @classmethod
+    def empty(cls, *, num_rows: int, max_pages: int, num_pages: int, page_size: int, device="cuda") -> "PagePool":
+        """A pool without tokens."""
+        zeros = lambda *shape: torch.zeros(shape, dtype=torch.int32, device=device)  # noqa: E731
+        return cls(zeros(num_rows, max_pages), zeros(num_rows), zeros(num_pages), page_size=page_size)
+
+    def _index(self, *tensors):
+        _here(torch.cuda.current_device(), self.table)
+        n = tensors[0].numel()
+        for t in tensors:
+            if t.dtype != torch.int32 or not t.is_contiguous() or t.numel() != n or t.device != self.table.device:
+                raise ValueError("index arrays must be contiguous CUDA int32 tensors of one length, on the pool's device")
+        return n
+
+    def extend(self, rows: torch.Tensor, add: torch.Tensor, total: Optional[int] = None,
+               slots: Optional[torch.Tensor] = None, stream=None):
+        """rows[i] grows by add[i] tokens. With `total`, the sum of add, the new tokens' int64
+        slots are returned, entry after entry."""
+        n = self._index(rows, add)
+        if slots is None and total is not None:
+            slots = torch.empty(total, dtype=torch.int64, device=self.table.device)
+        elif slots is not None:
+            _want(slots, "slots", torch.int64)
+        _check(self._lib.pkv_pages_extend(self._desc, rows.data_ptr(), add.data_ptr(), n,
+                                          None if slots is None else slots.data_ptr(),
+                                          0 if slots is None else slots.numel(), _stream_handle(stream)),
+               "pkv_pages_extend")
+        return slots
+
+    def fork(self, parents: torch.Tensor, children: torch.Tensor, src: Optional[torch.Tensor] = None,
+             dst: Optional[torch.Tensor] = None, stream=None):
+        """children[i], an empty row, becomes a copy of parents[i]: full pages are shared, a
+        partly filled last one is new. Returns (src, dst), the pages to copy (or -1)."""
+        n = self._index(parents, children)
+        src = torch.empty_like(parents) if src is None else src
+        dst = torch.empty_like(parents) if dst is None else dst
+        self._index(src, dst, parents)
+        _check(self._lib.pkv_pages_fork(self._desc, parents.data_ptr(), children.data_ptr(), n, src.data_ptr(),
+                                        dst.data_ptr(), _stream_handle(stream)), "pkv_pages_fork")
+        return src, dst
+
+    def free(self, rows: torch.Tensor, stream=None):
+        """The rows become empty; pages that no other row names are free again."""
+        n = self._index(rows)
+        _check(self._lib.pkv_pages_free(self._desc, rows.data_ptr(), n, _stream_handle(stream)), "pkv_pages_free")
+
+    def compact(self, out: Optional["PagePool"] = None, src: Optional[torch.Tensor] = None,
+                dst: Optional[torch.Tensor] = None, count: Optional[torch.Tensor] = None, stream=None):
+        """The pages in use move to the lowest ids; the new table, lens and refs go to `out`
+        (None: in place). Returns (src, dst, count): the pages to copy, and how many on the
+        device. The caches' pages are the caller's to copy (copy_pages) before the new
+        table is used."""
+        if src is None:
+            src = torch.empty(self.refs.shape[0] // 2, dtype=torch.int32, device=self.table.device)
+        if dst is None:
+            dst = torch.empty_like(src)
+        if count is None:
+            count = torch.empty(1, dtype=torch.int32, device=self.table.device)
+        n = self._index(src, dst)
+        self._index(count)
+        _check(self._lib.pkv_pages_compact(self._desc, (out or self)._desc, src.data_ptr(), dst.data_ptr(), n,
+                                           count.data_ptr(), _stream_handle(stream)), "pkv_pages_compact")
+        return src, dst, count
+
+    def device_status(self) -> int:
+        """Read and clear what earlier calls recorded (waits for the device)."""
+        torch.cuda.synchronize(self.table.device)
+        st = int(self._status.item())
+        self._status.zero_()
+        return st
+
+
+def copy_pages(k_cache: torch.Tensor, v_cache: torch.Tensor, src: torch.Tensor, dst: torch.Tensor,
+               count: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None, stream=None):
+    """Page dst[i] of both caches becomes page src[i]. Caches [num_pages, P, H_kv, d], or
+    [layers, num_pages, P, H_kv, d] for every layer at once, contiguous, of any type; src
+    and dst int32, negative ids skipped; count: a device int32 of how many pairs are
+    meant (default: all)."""
+    lib = _lib or load_library()
+    if k_cache.shape != v_cache.shape or k_cache.dtype != v_cache.dtype or k_cache.dim() not in (4, 5):
+        raise ValueError("k_cache and v_cache must be [num_pages, P, H_kv, d] or [layers, num_pages, P, H_kv, d]")
+    if not (k_cache.is_cuda and k_cache.is_contiguous() and v_cache.is_cuda and v_cache.is_contiguous()):
+        raise ValueError("the caches must be contiguous CUDA tensors")
+    if src.shape != dst.shape:
+        raise ValueError("src and dst must have one length")
+    for t, name in ((src, "src"), (dst, "dst"), (count, "count"), (status, "status")):
+        _want(t, name, torch.int32)
+    _here(torch.cuda.current_device(), k_cache, v_cache, src, dst, count, status)
+    layers = k_cache.shape[0] if k_cache.dim() == 5 else 1
+    pages = k_cache.shape[-4]
+    layer_bytes = k_cache.numel() * k_cache.element_size() // layers if layers else 0
+    _check(lib.pkv_copy_pages(k_cache.data_ptr(), v_cache.data_ptr(), layers, layer_bytes, pages,
+                              layer_bytes // pages if pages else 0, src.data_ptr(), dst.data_ptr(), src.numel(),
+                              None if count is None else count.data_ptr(), None if status is None else status.data_ptr(),
+                              _stream_handle(stream)), "pkv_copy_pages")
 
 
 def plan(**kw) -> Plan:

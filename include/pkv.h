@@ -440,14 +440,15 @@ PKV_API int pkv_pages_workspace(int32_t num_rows, int32_t num_pages, int64_t *by
 /*
  * Every result of the calls below is a function of their inputs alone: new pages are the
  * lowest free ids, handed out in the order of the call's entries and, within one, of its
- * pages. A call whose inputs do not fit changes nothing but its outputs, which it fills
- * with -1 (a slot or page id that pkv_norm_rope_append and pkv_copy_pages skip), and
- * records in pool->status PKV_ERR_OOM (not enough free pages) or PKV_ERR_DEVICE_BOUNDS (a
- * row out of range or named twice, a negative count, a length or row beyond row_stride
- * pages, a page id out of range or with refs 0 in a row that is read, slots beyond their
- * capacity). Index arrays are DEVICE int32; n is at most num_rows. Asynchronous on
- * `stream`, one launch each (compact: two), nothing is allocated; capturable. They return
- * PKV_OK, PKV_ERR_INVALID_ARG, PKV_ERR_UNSUPPORTED (sizes near 2^31) or PKV_ERR_CUDA.
+ * pages. An extend or fork whose entries do not fit changes nothing but its outputs, which
+ * it fills with -1 (a slot or page id that pkv_norm_rope_append and pkv_copy_pages skip),
+ * and records in pool->status PKV_ERR_DEVICE_BOUNDS (a row out of range or named twice, a
+ * negative count, a length beyond row_stride pages, slots beyond their capacity) or
+ * PKV_ERR_OOM (not enough free pages). Table entries in use that are no page ids (a table
+ * that these calls did not write) are recorded as PKV_ERR_DEVICE_BOUNDS where they are
+ * met, and left as they are. Index arrays are DEVICE int32; n is at most num_rows.
+ * Asynchronous on `stream`, one or two launches, nothing is allocated; capturable. They
+ * return PKV_OK, PKV_ERR_INVALID_ARG, PKV_ERR_UNSUPPORTED (sizes near 2^31) or PKV_ERR_CUDA.
  *
  * pkv_pages_extend: rows[i] grows by add[i] tokens. slots (or NULL) gets, entry after
  * entry, each new token's slot page * page_size + offset, slots_capacity at most.
@@ -464,7 +465,11 @@ PKV_API int pkv_pages_extend(const pkv_page_pool *pool, const int32_t *rows, con
 PKV_API int pkv_pages_fork(const pkv_page_pool *pool, const int32_t *parents, const int32_t *children, int32_t n,
                            int32_t *src, int32_t *dst, void *stream);
 
-/* pkv_pages_free: the rows become empty; pages that no other row names are free again. */
+/*
+ * pkv_pages_free: the rows become empty; pages that no other row names are free again. A
+ * row named twice is freed once; one out of range, or whose length is not one, is recorded
+ * and skipped.
+ */
 PKV_API int pkv_pages_free(const pkv_page_pool *pool, const int32_t *rows, int32_t n, void *stream);
 
 /*

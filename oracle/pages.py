@@ -1,7 +1,8 @@
 """Plain Python model of the page pool (pkv_pages_*): lists and loops, from the definitions.
 
 A pool is (table, lens, refs, page_size); every call returns the new pool and its outputs,
-or raises Refused with the code the library records, the pool unchanged."""
+or raises Refused with the code the library records, the pool unchanged (free goes entry by
+entry and never refuses)."""
 from __future__ import annotations
 
 import numpy as np
@@ -26,13 +27,9 @@ class Pool:
     def pages(self, row):
         return -(-int(self.lens[row]) // self.P)
 
-    def _row(self, row, read):
+    def _row(self, row):
         if not 0 <= row < len(self.lens) or not 0 <= self.lens[row] or self.pages(row) > self.table.shape[1]:
             raise Refused(BOUNDS)
-        if read:
-            for page in self.table[row, : self.pages(row)]:
-                if not 0 <= page < len(self.refs) or self.refs[page] <= 0:
-                    raise Refused(BOUNDS)
 
     def _take(self, need):
         ids = [i for i in range(len(self.refs)) if self.refs[i] == 0][:need]
@@ -43,7 +40,7 @@ class Pool:
     def extend(self, rows, add, capacity=None):
         rows, add = [int(r) for r in rows], [int(a) for a in add]
         for r, a in zip(rows, add):
-            self._row(r, False)
+            self._row(r)
             if a < 0 or -(-(int(self.lens[r]) + a) // self.P) > self.table.shape[1]:
                 raise Refused(BOUNDS)
         if len(set(rows)) < len(rows) or (capacity is not None and sum(add) > capacity):
@@ -61,8 +58,8 @@ class Pool:
     def fork(self, parents, children):
         parents, children = [int(p) for p in parents], [int(c) for c in children]
         for p, c in zip(parents, children):
-            self._row(c, False)
-            self._row(p, True)
+            self._row(c)
+            self._row(p)
             if self.lens[c] != 0:
                 raise Refused(BOUNDS)
         if len(set(children)) < len(children):
@@ -83,15 +80,21 @@ class Pool:
         return new, src, dst
 
     def free(self, rows):
-        rows = [int(r) for r in rows]
-        for r in rows:
-            self._row(r, True)
-        if len(set(rows)) < len(rows):
-            raise Refused(BOUNDS)
+        """Entry by entry: self.bad counts the rows that are skipped and the ids and counts
+        that are not what they should be."""
         new = self.copy()
-        for r in rows:
-            for page in self.table[r, : self.pages(r)]:
-                new.refs[page] -= 1
+        new.bad = 0
+        for r in (int(r) for r in rows):
+            try:
+                new._row(r)
+            except Refused:
+                new.bad += 1
+                continue
+            for page in self.table[r, : new.pages(r)]:
+                if 0 <= page < len(self.refs) and new.refs[page] > 0:
+                    new.refs[page] -= 1
+                else:
+                    new.bad += 1
             new.lens[r] = 0
         return new
 

@@ -10,15 +10,17 @@
 //           not full is one the child will write, so it gets a free one and (src, dst)
 //   free:   refs - 1 for the row's pages, len = 0
 //   compact: with n live pages, the live ids >= n move to the free ids < n, both ascending
-// A call that meets an input it cannot take (a row or page out of range, a row named twice,
-// not enough free pages) changes nothing and records why.
+// extend and fork take their entries together: if one does not fit (a row out of range or
+// named twice, no page left) the call changes nothing and records why.
 //
-// extend, fork and free are one launch each of one cluster of 8 CTAs: the free pages have
-// to be ranked, a scan over refs, and the cluster's barriers and shared memories do in one
-// launch what would otherwise be three (count, scan, assign) or a scan of CTAs that spin on
-// one another. Every warp counts a segment of its own, the 256 counts are exchanged, and a
+// Free pages have to be ranked, a scan over refs. rank_kernel does it, with the entries'
+// own prefix sums and checks, as one cluster of 8 CTAs, whose barriers and shared memories
+// spare the second and third launch of a scan over the grid, or CTAs that spin on one
+// another: every warp counts a segment of its own, the 256 counts are exchanged, and a
 // second pass over the segment (now in L2) writes the ids of the ranks that are wanted.
-// Bound by latency: four barriers' worth of dependent loads, over 4 bytes a page.
+// What it found is applied by a CTA to each entry over the whole GPU: on the cluster's 8
+// SMs alone, extending 256 rows by 512 thousand tokens took 33 us, now APPLY_TIMES.
+// Bound by latency: chains of dependent loads, over 4 bytes a page and entry.
 #include <cooperative_groups.h>
 
 #include <string>
@@ -36,6 +38,9 @@ constexpr int kCtas = 8;  // portable cluster size
 constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
 constexpr int kAllWarps = kCtas * kWarps;
+constexpr int kDeep = 4;  // 16-byte loads that a lane keeps in flight over refs
+constexpr int kApplyThreads = 256;
+constexpr int32_t kBad = 1, kTooMany = 2;  // of the verdict word
 
 struct PoolParams {
     int32_t *table, *lens, *refs;
@@ -48,7 +53,7 @@ struct PoolParams {
     int64_t *first_slot; // [num_rows] its first slot in the call's slots (fork: the parent's length,
                          // which a child's may replace when a row is both)
     int32_t *free_ids;   // [num_pages] the free pages by rank (compact: a page's rank)
-    int32_t *word;       // compact: the live pages
+    int32_t *word;       // extend, fork: what does not fit; compact: the live pages
 };
 
 __device__ __forceinline__ int ceil_div(int64_t x, int p) { return (int)((x + p - 1) / p); }
@@ -58,7 +63,6 @@ struct Board {
     int32_t pages[kWarps];   // by warp: new pages, free pages, new tokens of its segment
     int32_t frees[kWarps];
     long long tokens[kWarps];
-    int32_t error;
     // every warp's, after the exchange
     int32_t all_pages[kAllWarps];
     int32_t all_frees[kAllWarps];
@@ -128,9 +132,17 @@ __device__ __forceinline__ int count_free(const int4 &r) { return (r.x == 0) + (
 // Free pages of [lo, hi), which starts at a multiple of 4.
 __device__ int segment_free(const int32_t *refs, int lo, int hi, int lane)
 {
-    int n = 0;
-#pragma unroll 4
-    for (int p = lo + 4 * lane; p < hi; p += 128)
+    int n = 0, base = lo;
+    for (; base + 128 * kDeep <= hi; base += 128 * kDeep) {
+        int4 r[kDeep];
+#pragma unroll
+        for (int u = 0; u < kDeep; ++u)
+            r[u] = __ldcg(reinterpret_cast<const int4 *>(refs + base + 128 * u) + lane);
+#pragma unroll
+        for (int u = 0; u < kDeep; ++u)
+            n += count_free(r[u]);
+    }
+    for (int p = base + 4 * lane; p < hi; p += 128)
         n += count_free(refs4(refs, p, hi));
     return warp_sum(n);
 }
@@ -139,23 +151,29 @@ __device__ int segment_free(const int32_t *refs, int lo, int hi, int lane)
 // free_ids[rank], as far as ranks below `want` go.
 __device__ void write_free(const PoolParams &p, int lo, int hi, int rank, int want, int lane)
 {
-    for (int base = lo; base < hi && rank < want; base += 128) {
-        const int at = base + 4 * lane;
-        const int4 r = refs4(p.refs, at, hi);
-        const int n = count_free(r), before = warp_before(n, lane);
-        int k = rank + before;
-        if (r.x == 0 && k < want)
-            p.free_ids[k] = at;
-        k += r.x == 0;
-        if (r.y == 0 && k < want)
-            p.free_ids[k] = at + 1;
-        k += r.y == 0;
-        if (r.z == 0 && k < want)
-            p.free_ids[k] = at + 2;
-        k += r.z == 0;
-        if (r.w == 0 && k < want)
-            p.free_ids[k] = at + 3;
-        rank += __shfl_sync(0xffffffffu, before + n, 31);
+    for (int base = lo; base < hi && rank < want; base += 128 * kDeep) {
+        int4 r[kDeep];
+#pragma unroll
+        for (int u = 0; u < kDeep; ++u)
+            r[u] = refs4(p.refs, base + 128 * u + 4 * lane, hi);
+#pragma unroll
+        for (int u = 0; u < kDeep; ++u) {
+            const int at = base + 128 * u + 4 * lane;
+            const int n = count_free(r[u]), before = warp_before(n, lane);
+            int k = rank + before;
+            if (r[u].x == 0 && k < want)
+                p.free_ids[k] = at;
+            k += r[u].x == 0;
+            if (r[u].y == 0 && k < want)
+                p.free_ids[k] = at + 1;
+            k += r[u].y == 0;
+            if (r[u].z == 0 && k < want)
+                p.free_ids[k] = at + 2;
+            k += r[u].z == 0;
+            if (r[u].w == 0 && k < want)
+                p.free_ids[k] = at + 3;
+            rank += __shfl_sync(0xffffffffu, before + n, 31);
+        }
     }
 }
 
@@ -188,29 +206,6 @@ __device__ __forceinline__ void before_and_total(const T *all, int gw, int lane,
     total = warp_sum64(t);
 }
 
-// Whether any CTA met an error (behind a cluster barrier; the caller passes another one
-// before it exits).
-__device__ bool any_error(cg::cluster_group &cluster, Board &b)
-{
-    int e = 0;
-    if (threadIdx.x < kCtas)
-        e = *cluster.map_shared_rank(&b.error, threadIdx.x);
-    return __syncthreads_or(e);
-}
-
-// Whether the entries in use of a row of `len` tokens are page ids, with refs when
-// `counted`; the lanes of a warp share the row.
-__device__ bool row_fine(const PoolParams &p, int row, int64_t len, bool counted, int lane)
-{
-    const int n = ceil_div(len, p.page_size);
-    bool ok = true;
-    for (int k = lane; k < n; k += 32) {
-        const int page = p.table[row * p.row_stride + k];
-        ok = ok && (unsigned)page < (unsigned)p.num_pages && (!counted || p.refs[page] > 0);
-    }
-    return __all_sync(0xffffffffu, ok);
-}
-
 __device__ __forceinline__ bool len_fine(const PoolParams &p, int64_t len)
 {
     return len >= 0 && ceil_div(len, p.page_size) <= p.row_stride;
@@ -218,26 +213,26 @@ __device__ __forceinline__ bool len_fine(const PoolParams &p, int64_t len)
 
 enum Op { kExtend, kFork };
 
-// kExtend: rows, add, slots. kFork: rows = children, add = parents, src, dst.
+// Rank the pages and slots of a call's entries, and the free pages; the verdict word says
+// whether the call can be done. kExtend: rows, add. kFork: rows = children, add = parents.
 template <Op OP>
-__global__ void __launch_bounds__(kThreads) grow_kernel(const PoolParams p, const int32_t *rows, const int32_t *add, int n,
-                                                        int64_t *slots, int64_t slots_capacity, int32_t *src,
-                                                        int32_t *dst)
+__global__ void __launch_bounds__(kThreads) rank_kernel(const PoolParams p, const int32_t *rows, const int32_t *add, int n,
+                                                        bool slots, int64_t slots_capacity)
 {
     __shared__ Board b;
     cg::cluster_group cluster = cg::this_cluster();
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, gw = (int)cluster.block_rank() * kWarps + warp;
     const int P = p.page_size;
-    if (threadIdx.x == 0)
-        b.error = 0;
-    __syncthreads();
     grid_dependency_wait();
     grid_launch_dependents();
+    if (gw == 0 && lane == 0)
+        *p.word = 0;
 
     // What each entry of the warp's segment needs, and the free pages of its segment.
     int e_lo, e_hi, p_lo, p_hi;
     segment(n, 1, gw, e_lo, e_hi);
     segment(p.num_pages, 4, gw, p_lo, p_hi);
+    const int frees = segment_free(p.refs, p_lo, p_hi, lane);
     auto need_of = [&](int i, long long &tokens) -> int {
         tokens = 0;
         if (i >= e_hi)
@@ -257,16 +252,17 @@ __global__ void __launch_bounds__(kThreads) grow_kernel(const PoolParams p, cons
         const int parent = add[i];
         if ((unsigned)parent >= (unsigned)p.num_rows || len != 0)
             return -1;
-        const int64_t from = p.lens[parent];
-        return len_fine(p, from) ? from % P != 0 : -1;
+        tokens = p.lens[parent];
+        return len_fine(p, tokens) ? tokens % P != 0 : -1;
     };
     long long pages = 0, tokens = 0;
+    bool bad = false;
     for (int i0 = e_lo; i0 < e_hi; i0 += 32) {
         const int i = i0 + lane;
         long long t;
         const int need = need_of(i, t);
         if (need < 0)
-            b.error = 1;
+            bad = true;
         else if (i < e_hi)
             p.claim[rows[i]] = i;
         pages += max(need, 0);
@@ -274,19 +270,8 @@ __global__ void __launch_bounds__(kThreads) grow_kernel(const PoolParams p, cons
     }
     pages = warp_sum64(pages);
     tokens = warp_sum64(tokens);
-    if (pages > p.num_pages)  // more than there are: too many in any case
-        pages = p.num_pages + 1;
-    if (OP == kFork) {
-        for (int i = e_lo; i < e_hi; ++i) {
-            const int parent = add[i];
-            if ((unsigned)parent >= (unsigned)p.num_rows || !len_fine(p, p.lens[parent]) ||
-                !row_fine(p, parent, p.lens[parent], true, lane))
-                b.error = 1;
-        }
-    }
-    const int frees = segment_free(p.refs, p_lo, p_hi, lane);
     if (lane == 0) {
-        b.pages[warp] = (int32_t)pages;
+        b.pages[warp] = (int32_t)min(pages, p.num_pages + 1LL);  // more than there are: too many in any case
         b.frees[warp] = frees;
         b.tokens[warp] = tokens;
     }
@@ -297,9 +282,7 @@ __global__ void __launch_bounds__(kThreads) grow_kernel(const PoolParams p, cons
     before_and_total(b.all_pages, gw, lane, page_at, want);
     before_and_total(b.all_frees, gw, lane, rank, there);
     before_and_total(b.all_tokens, gw, lane, token_at, all_tokens);
-    const bool too_many = want > there;
-    const bool no_room = OP == kExtend && slots && all_tokens > slots_capacity;
-    if (!too_many)
+    if (want <= there)
         write_free(p, p_lo, p_hi, (int)rank, (int)want, lane);
     for (int i0 = e_lo; i0 < e_hi; i0 += 32) {
         const int i = i0 + lane;
@@ -309,125 +292,146 @@ __global__ void __launch_bounds__(kThreads) grow_kernel(const PoolParams p, cons
         const long long t_before = warp_before64(t, lane);
         if (i < e_hi) {
             p.first[i] = (int32_t)(page_at + before);
-            const int row = rows[i], parent = OP == kFork ? add[i] : 0;
-            if (OP == kExtend)
-                p.first_slot[i] = token_at + t_before;
-            else if ((unsigned)parent < (unsigned)p.num_rows)
-                p.first_slot[i] = p.lens[parent];
+            p.first_slot[i] = OP == kExtend ? token_at + t_before : t;
+            const int row = rows[i];
             if ((unsigned)row < (unsigned)p.num_rows && __ldcg(p.claim + row) != i)
-                b.error = 1;  // another entry names the row too
+                bad = true;  // another entry names the row too
         }
         page_at += __shfl_sync(0xffffffffu, before + need, 31);
         token_at += __shfl_sync(0xffffffffu, t_before + t, 31);
     }
-    cluster.sync();
-
-    const bool bad = any_error(cluster, b);
-    if (bad || too_many || no_room) {
-        // nothing changes; the outputs say "no page", which the calls that take them skip
-        if (gw == 0 && lane == 0)
-            record_status(p.status, bad || no_room ? PKV_ERR_DEVICE_BOUNDS : PKV_ERR_OOM);
-        const int64_t at = (int64_t)gw * 32 + lane;
-        if (OP == kFork)
-            for (int64_t i = at; i < n; i += kAllWarps * 32)
-                src[i] = dst[i] = -1;
-        else if (slots)
-            for (int64_t i = at; i < slots_capacity; i += kAllWarps * 32)
-                slots[i] = -1;
-    } else if (OP == kExtend) {
-        for (int i = gw; i < n; i += kAllWarps) {
-            const int row = rows[i], len = p.lens[row], more = add[i];
-            const int have = ceil_div(len, P), upto = ceil_div((int64_t)len + more, P);
-            int32_t *entries = p.table + row * p.row_stride;
-            const int32_t *fresh = p.free_ids + __ldcg(p.first + i);
-            for (int k = have + lane; k < upto; k += 32) {
-                const int page = __ldcg(fresh + k - have);
-                entries[k] = page;
-                p.refs[page] = 1;
-            }
-            if (slots) {
-                int64_t *out = slots + __ldcg(p.first_slot + i);
-                const int last = have > 0 ? entries[have - 1] : 0;  // filled up first
-                for (int t = lane; t < more; t += 32) {
-                    const int at = len + t, k = (unsigned)at / (unsigned)P;
-                    const int page = k < have ? last : __ldcg(fresh + k - have);
-                    out[t] = (int64_t)page * P + (at - k * P);
-                }
-            }
-            __syncwarp();  // every lane has the row's old length
-            if (lane == 0)
-                p.lens[row] = len + more;
-        }
-    } else {
-        for (int i = gw; i < n; i += kAllWarps) {
-            const int child = rows[i], parent = add[i], len = (int)__ldcg(p.first_slot + i);
-            const int full = len / P;
-            const int32_t *from = p.table + parent * p.row_stride;
-            int32_t *to = p.table + child * p.row_stride;
-            for (int k = lane; k < full; k += 32) {
-                const int page = from[k];
-                to[k] = page;
-                atomicAdd(p.refs + page, 1);
-            }
-            if (lane == 0) {
-                int a = -1, z = -1;
-                if (len % P != 0) {
-                    a = from[full];
-                    z = __ldcg(p.free_ids + __ldcg(p.first + i));
-                    to[full] = z;
-                    p.refs[z] = 1;
-                }
-                src[i] = a;
-                dst[i] = z;
-                p.lens[child] = len;
-            }
-        }
-    }
+    if (bad || (OP == kExtend && slots && all_tokens > slots_capacity))
+        atomicOr(p.word, kBad);
+    if (gw == 0 && lane == 0 && want > there)
+        atomicOr(p.word, kTooMany);
     cluster.sync();  // no CTA leaves while another reads its board
 }
 
-__global__ void __launch_bounds__(kThreads) free_kernel(const PoolParams p, const int32_t *rows, int n)
+// Whether the ranked call can be done; if not, block 0 records why.
+__device__ bool granted(const PoolParams &p)
 {
-    __shared__ Board b;
-    cg::cluster_group cluster = cg::this_cluster();
-    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, gw = (int)cluster.block_rank() * kWarps + warp;
-    if (threadIdx.x == 0)
-        b.error = 0;
-    __syncthreads();
+    const int verdict = *p.word;
+    if (verdict && blockIdx.x == 0 && threadIdx.x == 0)
+        record_status(p.status, verdict & kBad ? PKV_ERR_DEVICE_BOUNDS : PKV_ERR_OOM);
+    return verdict == 0;
+}
+
+// One CTA an entry.
+__global__ void __launch_bounds__(kApplyThreads) extend_kernel(const PoolParams p, const int32_t *rows, const int32_t *add,
+                                                               int64_t *slots, int64_t slots_capacity)
+{
     grid_dependency_wait();
     grid_launch_dependents();
-    for (int i = gw; i < n; i += kAllWarps) {
-        const int row = rows[i];
-        if ((unsigned)row >= (unsigned)p.num_rows || !len_fine(p, p.lens[row]) ||
-            !row_fine(p, row, p.lens[row], true, lane))
-            b.error = 1;
-        else if (lane == 0)
-            p.claim[row] = i;
+    const int i = blockIdx.x, P = p.page_size;
+    if (!granted(p)) {
+        if (slots)  // no slot: the calls that take them skip it
+            for (int64_t k = (int64_t)i * kApplyThreads + threadIdx.x; k < slots_capacity;
+                 k += (int64_t)gridDim.x * kApplyThreads)
+                slots[k] = -1;
+        return;
     }
-    cluster.sync();
-    for (int i = gw * 32 + lane; i < n; i += kAllWarps * 32)
-        if ((unsigned)rows[i] < (unsigned)p.num_rows && __ldcg(p.claim + rows[i]) != i)
-            b.error = 1;
-    cluster.sync();
-    if (any_error(cluster, b)) {
-        if (gw == 0 && lane == 0)
-            record_status(p.status, PKV_ERR_DEVICE_BOUNDS);
-    } else {
-        for (int i = gw; i < n; i += kAllWarps) {
-            const int row = rows[i], pages = ceil_div(p.lens[row], p.page_size);
-            for (int k = lane; k < pages; k += 32) {
-                int32_t *r = p.refs + p.table[row * p.row_stride + k];
-                if (atomicSub(r, 1) <= 0) {  // more entries named the page than were counted
-                    atomicAdd(r, 1);
-                    record_status(p.status, PKV_ERR_DEVICE_BOUNDS);
-                }
+    const int row = rows[i], len = p.lens[row], more = add[i];
+    const int have = ceil_div(len, P), upto = ceil_div((int64_t)len + more, P);
+    int32_t *entries = p.table + row * p.row_stride;
+    const int32_t *fresh = p.free_ids + p.first[i];
+    if (slots) {
+        int64_t *out = slots + p.first_slot[i];
+        const int last = have > 0 ? entries[have - 1] : 0;  // filled up first
+        constexpr int U = 4;  // tokens of a thread in flight
+        for (int64_t t0 = threadIdx.x; t0 < more; t0 += U * kApplyThreads) {
+            int page[U], in[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int64_t t = t0 + u * kApplyThreads;
+                const unsigned at = (unsigned)(len + t);
+                const int k = at / (unsigned)P;
+                in[u] = at - (unsigned)k * P;
+                page[u] = k < have ? last : t < more ? fresh[k - have] : 0;
             }
-            __syncwarp();
-            if (lane == 0)
-                p.lens[row] = 0;
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (t0 + u * kApplyThreads < more)
+                    out[t0 + u * kApplyThreads] = (int64_t)page[u] * P + in[u];
         }
     }
-    cluster.sync();
+    for (int64_t k = (int64_t)have + threadIdx.x; k < upto; k += kApplyThreads) {
+        const int page = fresh[k - have];
+        entries[k] = page;
+        p.refs[page] = 1;
+    }
+    __syncthreads();  // every thread has the row's old length
+    if (threadIdx.x == 0)
+        p.lens[row] = len + more;
+}
+
+__global__ void __launch_bounds__(kApplyThreads) fork_kernel(const PoolParams p, const int32_t *children,
+                                                             const int32_t *parents, int32_t *src, int32_t *dst)
+{
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int i = blockIdx.x;
+    if (!granted(p)) {
+        if (threadIdx.x == 0)
+            src[i] = dst[i] = -1;
+        return;
+    }
+    const int child = children[i], len = (int)p.first_slot[i], full = len / p.page_size;
+    const int32_t *from = p.table + parents[i] * p.row_stride;
+    int32_t *to = p.table + child * p.row_stride;
+    for (int k = threadIdx.x; k < full; k += kApplyThreads) {
+        const int page = from[k];
+        to[k] = page;
+        if ((unsigned)page < (unsigned)p.num_pages)
+            atomicAdd(p.refs + page, 1);
+        else
+            record_status(p.status, PKV_ERR_DEVICE_BOUNDS);
+    }
+    if (threadIdx.x == 0) {
+        int a = -1, z = -1;
+        if (len % p.page_size != 0) {
+            a = from[full];
+            z = p.free_ids[p.first[i]];
+            to[full] = z;
+            p.refs[z] = 1;
+            if ((unsigned)a >= (unsigned)p.num_pages) {
+                a = z = -1;
+                record_status(p.status, PKV_ERR_DEVICE_BOUNDS);
+            }
+        }
+        src[i] = a;
+        dst[i] = z;
+        p.lens[child] = len;
+    }
+}
+
+// One CTA an entry, each taken by itself: whoever finds a row's length gives its pages
+// back, so that a row named twice is freed once.
+__global__ void __launch_bounds__(kApplyThreads) free_kernel(const PoolParams p, const int32_t *rows)
+{
+    __shared__ int shared_len;
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int row = rows[blockIdx.x];
+    if (threadIdx.x == 0) {
+        int len = 0;
+        if ((unsigned)row < (unsigned)p.num_rows && len_fine(p, p.lens[row]))
+            len = atomicExch(p.lens + row, 0);
+        else
+            record_status(p.status, PKV_ERR_DEVICE_BOUNDS);
+        shared_len = len;
+    }
+    __syncthreads();
+    const int pages = ceil_div(shared_len, p.page_size);
+    const int32_t *entries = p.table + row * p.row_stride;
+    for (int k = threadIdx.x; k < pages; k += kApplyThreads) {
+        const int page = entries[k];
+        if ((unsigned)page >= (unsigned)p.num_pages) {
+            record_status(p.status, PKV_ERR_DEVICE_BOUNDS);
+        } else if (atomicSub(p.refs + page, 1) <= 0) {  // more entries named the page than were counted
+            atomicAdd(p.refs + page, 1);
+            record_status(p.status, PKV_ERR_DEVICE_BOUNDS);
+        }
+    }
 }
 
 // The moves of a compaction: src, dst, their number, refs_out, and in the workspace each
@@ -761,8 +765,11 @@ PKV_API int pkv_pages_extend(const pkv_page_pool *pool, const int32_t *rows, con
         return refuse(PKV_ERR_INVALID_ARG, "pkv_pages_extend", "slots are misaligned or their capacity negative");
     if (n == 0)
         return PKV_OK;
-    return launched("pkv_pages_extend", launch(grow_kernel<kExtend>, kCtas, kThreads, kCtas, stream, p, rows, add, n,
-                                               slots, slots_capacity, (int32_t *)nullptr, (int32_t *)nullptr));
+    cudaError_t ce = launch(rank_kernel<kExtend>, kCtas, kThreads, kCtas, stream, p, rows, add, (int)n, slots != nullptr,
+                            slots_capacity);
+    if (ce == cudaSuccess)
+        ce = launch(extend_kernel, n, kApplyThreads, 1, stream, p, rows, add, slots, slots_capacity);
+    return launched("pkv_pages_extend", ce);
 }
 
 PKV_API int pkv_pages_fork(const pkv_page_pool *pool, const int32_t *parents, const int32_t *children, int32_t n,
@@ -779,8 +786,11 @@ PKV_API int pkv_pages_fork(const pkv_page_pool *pool, const int32_t *parents, co
         st = take_entries("pkv_pages_fork", p, n, src, dst);
     if (st != PKV_OK || n == 0)
         return st;
-    return launched("pkv_pages_fork", launch(grow_kernel<kFork>, kCtas, kThreads, kCtas, stream, p, children, parents, n,
-                                             (int64_t *)nullptr, (int64_t)0, src, dst));
+    cudaError_t ce = launch(rank_kernel<kFork>, kCtas, kThreads, kCtas, stream, p, children, parents, (int)n, false,
+                            (int64_t)0);
+    if (ce == cudaSuccess)
+        ce = launch(fork_kernel, n, kApplyThreads, 1, stream, p, children, parents, src, dst);
+    return launched("pkv_pages_fork", ce);
 }
 
 PKV_API int pkv_pages_free(const pkv_page_pool *pool, const int32_t *rows, int32_t n, void *stream)
@@ -794,7 +804,7 @@ PKV_API int pkv_pages_free(const pkv_page_pool *pool, const int32_t *rows, int32
         st = take_entries("pkv_pages_free", p, n, rows, rows);
     if (st != PKV_OK || n == 0)
         return st;
-    return launched("pkv_pages_free", launch(free_kernel, kCtas, kThreads, kCtas, stream, p, rows, n));
+    return launched("pkv_pages_free", launch(free_kernel, n, kApplyThreads, 1, stream, p, rows));
 }
 
 PKV_API int pkv_pages_compact(const pkv_page_pool *pool, const pkv_page_pool *out, int32_t *src, int32_t *dst,

@@ -165,27 +165,51 @@ def test_a_row_that_is_parent_and_child(pkv):
         assert out and model.lens[2] == 0
 
 
-@pytest.mark.parametrize("rows", [[0, 0], [3, 8], [-1], [0, 3, 5, 6, 0]])
-def test_free_refuses_and_leaves_the_pool(pkv, rows):
+@pytest.mark.parametrize("rows", [[0, 0], [3, 8], [-1], [0, 3, 5, 6, 0], [2 ** 31 - 1, 6]])
+def test_free_takes_each_row_by_itself(pkv, rows):
+    """A row named twice is freed once, one that is none is recorded."""
     pool, model = _filled(pkv)
-    _both(lambda: pool.free(_dev(rows)), lambda: model.free(rows), pool, model, "free")
+    pool.free(_dev(rows))
+    model = model.free(rows)
+    assert pool.device_status() == (pkv.PKV_ERR_DEVICE_BOUNDS if model.bad else 0)
+    _same(pool, model, "free")
 
 
-def test_broken_tables_are_refused(pkv):
-    """Ids out of range and pages nobody counted: recorded, nothing is done."""
+def test_broken_tables_are_recorded(pkv):
+    """Ids out of range, pages nobody counted and lengths that are none: recorded where they
+    are met, never followed."""
     for value in (-1, 30, 2 ** 31 - 1, 29):  # 29 is in range but free
         pool, model = _filled(pkv)
         pool.table[0, 1] = value
         model.table[0, 1] = value
-        _both(lambda: pool.free(_dev([3, 0])), lambda: model.free([3, 0]), pool, model, "free")
-        _both(lambda: pool.fork(_dev([0]), _dev([1])), lambda: model.fork([0], [1]), pool, model, "fork")
         pool.compact()  # packs the rest; the entry stays what it is
         assert pool.device_status() == pkv.PKV_ERR_DEVICE_BOUNDS
         assert pool.table[0, 1] == value and torch.equal(pool.lens, _dev(model.lens))
+        pool, model = _filled(pkv)
+        pool.table[0, 1] = value
+        model.table[0, 1] = value
+        src, dst = pool.fork(_dev([0]), _dev([1]))
+        assert pool.device_status() == (0 if value == 29 else pkv.PKV_ERR_DEVICE_BOUNDS)
+        assert pool.table[1, 1] == value and src[0] == pool.table[0, 2] and pool.refs[dst[0]] == 1
+        pool.free(_dev([1, 3]))
+        assert pool.device_status() == (0 if value == 29 else pkv.PKV_ERR_DEVICE_BOUNDS)
+        pool.free(_dev([0]))  # here 29 has no count left to give
+        assert pool.device_status() == pkv.PKV_ERR_DEVICE_BOUNDS
+        _same(pool, Pool(pool.table.cpu().numpy(), *[getattr(model.free([3, 0]), x) for x in ("lens", "refs")], 4), "rest")
     pool, model = _filled(pkv)
-    pool.lens[3] = 25  # more than a row's six pages
-    model.lens[3] = 25
-    _both(lambda: pool.free(_dev([3])), lambda: model.free([3]), pool, model, "length")
+    pool.table[0, 2] = 99  # the page to copy
+    src, dst = pool.fork(_dev([0]), _dev([1]))
+    assert pool.device_status() == pkv.PKV_ERR_DEVICE_BOUNDS and src[0] == dst[0] == -1
+    for length in (25, -3):  # more than a row's six pages, and none
+        pool, model = _filled(pkv)
+        pool.lens[3] = length
+        model.lens[3] = length
+        pool.free(_dev([3, 6]))
+        model = model.free([3, 6])
+        assert model.bad == 1 and pool.device_status() == pkv.PKV_ERR_DEVICE_BOUNDS
+        _same(pool, model, "length")
+        _both(lambda: pool.fork(_dev([3]), _dev([1])), lambda: model.fork([3], [1]), pool, model, "fork")
+        _both(lambda: pool.extend(_dev([3]), _dev([0])), lambda: model.extend([3], [0]), pool, model, "extend")
 
 
 def test_compact_out_of_place_and_without_room(pkv):

@@ -45,7 +45,8 @@ def test_model_keeps_its_invariants():
                 empty = [r for r in some if pool.lens[r] == 0]
                 pool, _, _ = pool.fork(rng.integers(0, 12, size=len(empty)), empty)
             elif k == 2:
-                pool = pool.free(some)
+                pool = pool.free(some.tolist() + some.tolist())  # freed once
+                assert pool.bad == 0
             else:
                 pool, src, dst = pool.compact()
                 assert (pool.refs[: (pool.refs > 0).sum()] > 0).all()

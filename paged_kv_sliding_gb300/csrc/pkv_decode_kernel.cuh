@@ -158,8 +158,13 @@ __global__ void __launch_bounds__(DecTraits<D, TT, KV, TPW>::kThreads, DecTraits
     const int tid = threadIdx.x;
     const int warp = tid >> 5;
     const int lane = tid & 31;
-    if (p.live_items && (int)blockIdx.x >= *p.live_items)
-        return;  // a capturable plan's fixed grid: this CTA has no work item now
+    if (p.live_items && (int)blockIdx.x >= *p.live_items) {
+        // A capturable plan's fixed grid: this CTA has no work item now. It still waits: a
+        // grid that ended before the one ahead of it would let the one behind start too
+        // early, when no CTA has work.
+        grid_dependency_wait();
+        return;
+    }
     const DecodeItem it = p.items[blockIdx.x];
     struct {
         int32_t qo_begin, kv_len, kv_page_begin;

@@ -520,7 +520,7 @@ void build_schedule(const pkv_plan_desc &d, const std::vector<HostRequest> &reqs
         decode_tile = fixed_tile > 0 ? fixed_tile
                                      : decode_tile_for(d.head_dim,
                                                        d_items.empty() ? 0 : keys(d_items.front()),
-                                                       (int64_t)d_items.size(), device_sm_count(device));
+                                                       (int64_t)d_items.size(), device_sm_count(device), sinks > 0);
     }
     sc.num_partials = num_partials;
     sc.num_counters = num_counters;

@@ -202,12 +202,20 @@ cudaError_t launch_decode(const DecodeParams &p, int head_dim, int num_items, cu
 // short key ranges, which are latency-bound, and for medium ones (<= 1024 keys)
 // whose CTAs need more than one wave at 2 per SM but fit in one at 4; otherwise 64
 // (twice the bytes in flight per CTA, which long ranges need).
-inline int decode_tile_for(int head_dim, int64_t max_keys, int64_t n_items, int n_sm)
+// Plans with sinks have a rule of their own for the medium ranges, whose bound a window
+// of 1024 keys and its sinks would just miss: up to 1536 keys from 2.25 items per SM on,
+// 640 below. Measured, 32 against 64: 512 items of 1028 keys 41.1 / 45.2 us (E4M3 25.3 /
+// 32.2), 1405 keys 51.3 / 56.2, 352 items of 1028 keys 30.7 / 38.2; 512 items of 2005 keys
+// 62.6 / 61.5; 312 items of 505 keys 15.3 / 16.7, of 1028 keys 27.6 / 26.0 (E4M3 22.4 / 16.2).
+inline int decode_tile_for(int head_dim, int64_t max_keys, int64_t n_items, int n_sm, bool sinks = false)
 {
     if (head_dim > 128)
         return 64;
     if (max_keys <= 192)
         return 32;
+    if (sinks)
+        return n_items > 2LL * n_sm && n_items <= 4LL * n_sm && max_keys <= (4 * n_items > 9LL * n_sm ? 1536 : 640) ? 32
+                                                                                                                : 64;
     if (max_keys <= 1024 && n_items > 2LL * n_sm && n_items <= 4LL * n_sm)
         return 32;
     return 64;

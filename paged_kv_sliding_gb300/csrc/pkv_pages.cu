@@ -19,7 +19,7 @@
 // another: every warp counts a segment of its own, the 256 counts are exchanged, and a
 // second pass over the segment (now in L2) writes the ids of the ranks that are wanted.
 // What it found is applied by a CTA to each entry over the whole GPU: on the cluster's 8
-// SMs alone, extending 256 rows by 512 thousand tokens took 33 us, now APPLY_TIMES.
+// SMs alone, extending 256 rows by 512 thousand tokens took 33 us, now a tenth of it.
 // Bound by latency: chains of dependent loads, over 4 bytes a page and entry.
 #include <cooperative_groups.h>
 

@@ -242,6 +242,13 @@ __global__ void __launch_bounds__(384, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = tmem_base_s;
+    // With sinks the launch may overlap the end of the kernel before it (a persistent CTA
+    // starts where one of the last grid's has left): everything above reads the plan's own
+    // data only.
+    if (kSink) {
+        grid_dependency_wait();
+        grid_launch_dependents();
+    }
 
     // Register split: the block is launched with 384 x 168 registers (the build
     // checks that ptxas allocated exactly 168); the softmax warpgroups take 200 and
@@ -1335,6 +1342,19 @@ cudaError_t launch_pp_dmt(const PrefillParams &p, const CUtensorMap &tq, const C
         if (e != cudaSuccess)
             return e;
         configured = true;
+    }
+    if (MASK == kMaskCausalWindowSinks || MASK == kMaskWindowSinks) {
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3((unsigned)num_ctas);
+        cfg.blockDim = dim3(Tr::kThreads);
+        cfg.dynamicSmemBytes = Tr::kDynSmem;
+        cfg.stream = s;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        return cudaLaunchKernelEx(&cfg, prefill_pp_kernel<D, MASK, TMA_KV, RAGGED, KV>, p, tq, tk, tv, to);
     }
     prefill_pp_kernel<D, MASK, TMA_KV, RAGGED, KV><<<num_ctas, Tr::kThreads, Tr::kDynSmem, s>>>(p, tq, tk, tv, to);
     return cudaGetLastError();

@@ -560,6 +560,7 @@ class PagePool:
             _want(t, name, torch.int32)
         _here(torch.cuda.current_device(), table, lens, refs)
         self.table, self.lens, self.refs, self.page_size = table, lens, refs, int(page_size)
+        self._device = table.get_device()
         size = ctypes.c_int64()
         _check(self._lib.pkv_pages_workspace(table.shape[0], refs.shape[0], ctypes.byref(size)), "pkv_pages_workspace")
         self._workspace = torch.empty(size.value, dtype=torch.uint8, device=table.device)
@@ -577,10 +578,11 @@ class PagePool:
         return cls(zeros(num_rows, max_pages), zeros(num_rows), zeros(num_pages), page_size=page_size)
 
     def _index(self, *tensors):
-        _here(torch.cuda.current_device(), self.table)
+        if torch.cuda.current_device() != self._device:
+            raise ValueError(f"the pool is on cuda:{self._device}, which is not the current device")
         n = tensors[0].numel()
         for t in tensors:
-            if t.dtype != torch.int32 or not t.is_contiguous() or t.numel() != n or t.device != self.table.device:
+            if t.dtype != torch.int32 or not t.is_contiguous() or t.numel() != n or t.get_device() != self._device:
                 raise ValueError("index arrays must be contiguous CUDA int32 tensors of one length, on the pool's device")
         return n
 
@@ -603,10 +605,9 @@ class PagePool:
              dst: Optional[torch.Tensor] = None, stream=None):
         """children[i], an empty row, becomes a copy of parents[i]: full pages are shared, a
         partly filled last one is new. Returns (src, dst), the pages to copy (or -1)."""
-        n = self._index(parents, children)
         src = torch.empty_like(parents) if src is None else src
         dst = torch.empty_like(parents) if dst is None else dst
-        self._index(src, dst, parents)
+        n = self._index(parents, children, src, dst)
         _check(self._lib.pkv_pages_fork(self._desc, parents.data_ptr(), children.data_ptr(), n, src.data_ptr(),
                                         dst.data_ptr(), _stream_handle(stream)), "pkv_pages_fork")
         return src, dst
@@ -649,21 +650,28 @@ def copy_pages(k_cache: torch.Tensor, v_cache: torch.Tensor, src: torch.Tensor, 
     and dst int32, negative ids skipped; count: a device int32 of how many pairs are
     meant (default: all)."""
     lib = _lib or load_library()
-    if k_cache.shape != v_cache.shape or k_cache.dtype != v_cache.dtype or k_cache.dim() not in (4, 5):
+    shape, dev = k_cache.shape, torch.cuda.current_device()
+    if shape != v_cache.shape or k_cache.dtype != v_cache.dtype or len(shape) not in (4, 5):
         raise ValueError("k_cache and v_cache must be [num_pages, P, H_kv, d] or [layers, num_pages, P, H_kv, d]")
-    if not (k_cache.is_cuda and k_cache.is_contiguous() and v_cache.is_cuda and v_cache.is_contiguous()):
-        raise ValueError("the caches must be contiguous CUDA tensors")
+    if not (k_cache.is_contiguous() and v_cache.is_contiguous()):
+        raise ValueError("the caches must be contiguous")
     if src.shape != dst.shape:
         raise ValueError("src and dst must have one length")
-    for t, name in ((src, "src"), (dst, "dst"), (count, "count"), (status, "status")):
-        _want(t, name, torch.int32)
-    _here(torch.cuda.current_device(), k_cache, v_cache, src, dst, count, status)
-    layers = k_cache.shape[0] if k_cache.dim() == 5 else 1
-    pages = k_cache.shape[-4]
+    ptrs = []
+    for t in (src, dst, count, status):
+        if t is None:
+            ptrs.append(None)
+            continue
+        if t.dtype != torch.int32 or not t.is_contiguous() or t.get_device() != dev:
+            raise ValueError("src, dst, count and status must be contiguous int32 tensors on the current CUDA device")
+        ptrs.append(t.data_ptr())
+    if k_cache.get_device() != dev or v_cache.get_device() != dev:
+        raise ValueError("the caches must be on the current CUDA device")
+    layers = shape[0] if len(shape) == 5 else 1
+    pages = shape[-4]
     layer_bytes = k_cache.numel() * k_cache.element_size() // layers if layers else 0
     _check(lib.pkv_copy_pages(k_cache.data_ptr(), v_cache.data_ptr(), layers, layer_bytes, pages,
-                              layer_bytes // pages if pages else 0, src.data_ptr(), dst.data_ptr(), src.numel(),
-                              None if count is None else count.data_ptr(), None if status is None else status.data_ptr(),
+                              layer_bytes // pages if pages else 0, ptrs[0], ptrs[1], src.numel(), ptrs[2], ptrs[3],
                               _stream_handle(stream)), "pkv_copy_pages")
 
 

@@ -69,6 +69,13 @@ struct Board {
     long long all_tokens[kAllWarps];
 };
 
+// Neighbouring segments go to different CTAs: the lowest free pages, which a call wants, lie
+// in the first few (all in one CTA, ranking 32 thousand of them took 8 us longer).
+__device__ __forceinline__ int warp_of_cluster(const cg::cluster_group &cluster, int warp)
+{
+    return warp * kCtas + (int)cluster.block_rank();
+}
+
 __device__ __forceinline__ int32_t warp_sum(int32_t x) { return __reduce_add_sync(0xffffffffu, x); }
 
 __device__ __forceinline__ long long warp_sum64(long long x)
@@ -182,8 +189,8 @@ __device__ void exchange(cg::cluster_group &cluster, Board &b)
 {
     cluster.sync();
     if (threadIdx.x < kAllWarps) {
-        const Board *from = cluster.map_shared_rank(&b, threadIdx.x / kWarps);
-        const int w = threadIdx.x % kWarps;
+        const Board *from = cluster.map_shared_rank(&b, threadIdx.x % kCtas);
+        const int w = threadIdx.x / kCtas;
         b.all_pages[threadIdx.x] = from->pages[w];
         b.all_frees[threadIdx.x] = from->frees[w];
         b.all_tokens[threadIdx.x] = from->tokens[w];
@@ -221,7 +228,7 @@ __global__ void __launch_bounds__(kThreads) rank_kernel(const PoolParams p, cons
 {
     __shared__ Board b;
     cg::cluster_group cluster = cg::this_cluster();
-    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, gw = (int)cluster.block_rank() * kWarps + warp;
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, gw = warp_of_cluster(cluster, warp);
     const int P = p.page_size;
     grid_dependency_wait();
     grid_launch_dependents();
@@ -442,7 +449,7 @@ __global__ void __launch_bounds__(kThreads) moves_kernel(const PoolParams p, int
     __shared__ Board b;
     __shared__ int edge_live;  // live pages below n_live in the segment that n_live falls into
     cg::cluster_group cluster = cg::this_cluster();
-    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, gw = (int)cluster.block_rank() * kWarps + warp;
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, gw = warp_of_cluster(cluster, warp);
     grid_dependency_wait();
     grid_launch_dependents();
     int lo, hi;
@@ -466,10 +473,7 @@ __global__ void __launch_bounds__(kThreads) moves_kernel(const PoolParams p, int
     if (warp == 0) {
         int e_lo, e_hi;
         segment(p.num_pages, 4, edge, e_lo, e_hi);
-        int n = 0;
-        for (int q = e_lo + lane; q < min(e_hi, N); q += 32)
-            n += __ldcg(p.refs + q) != 0;
-        n = warp_sum(n);
+        const int n = max(min(e_hi, N) - e_lo, 0) - segment_free(p.refs, e_lo, min(e_hi, N), lane);
         if (lane == 0)
             edge_live = n;
     }
@@ -498,6 +502,8 @@ __global__ void __launch_bounds__(kThreads) moves_kernel(const PoolParams p, int
                 const int q = at + k;
                 if (q >= hi)
                     break;
+                if (refs_out != p.refs && (q >= N || r[k] != 0))  // what stays, and the ids given up
+                    refs_out[q] = q < N ? r[k] : 0;
                 if (r[k] == 0) {
                     if (q < N)
                         dst[fr] = q;
@@ -519,14 +525,6 @@ __global__ void __launch_bounds__(kThreads) moves_kernel(const PoolParams p, int
     cluster.sync();
     const int at = gw * 32 + lane;
     if (fits) {
-        if (refs_out != p.refs)  // what stays, and the ids that are given up
-            for (int q = at; q < p.num_pages; q += kAllWarps * 32) {
-                const int r = __ldcg(p.refs + q);
-                if (q >= N)
-                    refs_out[q] = 0;
-                else if (r != 0)
-                    refs_out[q] = r;
-            }
         for (int k = at; k < moves; k += kAllWarps * 32) {
             const int from = __ldcg(src + k);
             refs_out[__ldcg(dst + k)] = __ldcg(p.refs + from);
@@ -546,27 +544,26 @@ __global__ void __launch_bounds__(kThreads) moves_kernel(const PoolParams p, int
     cluster.sync();
 }
 
-// Table entries by the moves: one warp a row.
-__global__ void __launch_bounds__(256) rewrite_kernel(const PoolParams p, int32_t *table_out, int64_t out_stride,
+// Table entries by the moves: one CTA a row.
+constexpr int kRewriteThreads = 128;
+
+__global__ void __launch_bounds__(kRewriteThreads) rewrite_kernel(const PoolParams p, int32_t *table_out, int64_t out_stride,
                                                       int32_t *lens_out, const int32_t *dst)
 {
     grid_dependency_wait();
     grid_launch_dependents();
-    const int lane = threadIdx.x % 32;
-    const int row = blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32;
-    if (row >= p.num_rows)
-        return;
+    const int row = blockIdx.x;
     const int n_live = *p.word;
     const int64_t len = p.lens[row];
     if (!len_fine(p, len)) {
-        if (lane == 0)
+        if (threadIdx.x == 0)
             record_status(p.status, PKV_ERR_DEVICE_BOUNDS);
         return;
     }
     const int n = ceil_div(len, p.page_size);
     const int32_t *from = p.table + row * p.row_stride;
     int32_t *to = table_out + row * out_stride;
-    for (int k = lane; k < n; k += 32) {
+    for (int k = threadIdx.x; k < n; k += kRewriteThreads) {
         int page = from[k];
         if ((unsigned)page >= (unsigned)p.num_pages) {
             record_status(p.status, PKV_ERR_DEVICE_BOUNDS);
@@ -579,7 +576,7 @@ __global__ void __launch_bounds__(256) rewrite_kernel(const PoolParams p, int32_
         }
         to[k] = page;
     }
-    if (lane == 0 && lens_out != p.lens)
+    if (threadIdx.x == 0 && lens_out != p.lens)
         lens_out[row] = (int32_t)len;
 }
 
@@ -829,7 +826,7 @@ PKV_API int pkv_pages_compact(const pkv_page_pool *pool, const pkv_page_pool *ou
         return refuse(PKV_ERR_INVALID_ARG, "pkv_pages_compact", "src, dst and count are required");
     cudaError_t ce = launch(moves_kernel, kCtas, kThreads, kCtas, stream, p, o.refs, src, dst, (int)max_moves, count);
     if (ce == cudaSuccess && p.num_rows > 0)
-        ce = launch(rewrite_kernel, (p.num_rows + 7) / 8, 256, 1, stream, p, o.table, o.row_stride, o.lens,
+        ce = launch(rewrite_kernel, p.num_rows, kRewriteThreads, 1, stream, p, o.table, o.row_stride, o.lens,
                     (const int32_t *)dst);
     return launched("pkv_pages_compact", ce);
 }

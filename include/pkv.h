@@ -230,8 +230,9 @@ PKV_API int pkv_plan_create_capturable(pkv_plan **out, const pkv_plan_desc *desc
  * a key at or after p - window_left of one of its queries are not read, so their entries
  * in kv_indices may be anything (pages given back to a pool, say); a decode split over
  * several CTAs counts its splits over the visible keys.
- * As for plans without sinks, the V rows of a prefill's pages that hold a visible key
- * must be finite where the cache holds a key (an invisible one is weighed with 0).
+ * Prefill weighs the V rows of the pages it reads with 0 where a query does not see them,
+ * with and without sinks, so that those of the request's keys must be finite there; K
+ * may hold anything, as may both for decode.
  * Returns as pkv_plan_create; PKV_ERR_INVALID_ARG also for num_sinks < 0,
  * PKV_ERR_UNSUPPORTED for num_sinks > 2^24.
  */

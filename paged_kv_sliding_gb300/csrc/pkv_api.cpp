@@ -12,6 +12,7 @@
 #include <cmath>
 #include <cstdio>
 #include <cstring>
+#include <exception>
 #include <functional>
 #include <new>
 #include <queue>
@@ -611,6 +612,18 @@ void fill_image(const pkv_plan_desc &d, const Schedule &sc, const Layout &l, uin
     std::memcpy(img + l.live, &live, sizeof(live));
 }
 
+// No exception of the host containers leaves a C entry: a batch too large for them is out
+// of memory.
+template <typename F>
+int guarded(F &&body)
+{
+    try {
+        return body();
+    } catch (const std::exception &) {
+        return fail(PKV_ERR_OOM, "host allocation of the schedule failed");
+    }
+}
+
 }  // namespace
 
 extern "C" {
@@ -675,6 +688,8 @@ int create_plan(pkv_plan **out, const pkv_plan_desc *desc, const pkv_plan_caps *
                     (long long)sc.total_q, (long long)caps.total_q);
     const Layout lay = layout_for(d, caps);
 
+    std::vector<uint8_t> image(lay.upload, 0);
+    fill_image(d, sc, lay, image.data());
     pkv_plan *plan = new (std::nothrow) pkv_plan();
     if (!plan)
         return fail(PKV_ERR_OOM, "host allocation of the plan failed");
@@ -683,8 +698,6 @@ int create_plan(pkv_plan **out, const pkv_plan_desc *desc, const pkv_plan_caps *
         delete plan;
         return cuda_fail(ce, "cudaMalloc(plan workspace)");
     }
-    std::vector<uint8_t> image(lay.upload, 0);
-    fill_image(d, sc, lay, image.data());
     uint8_t *base = (uint8_t *)plan->workspace;
     ce = cudaMemcpyAsync(base, image.data(), lay.upload, cudaMemcpyHostToDevice, stream);
     if (ce == cudaSuccess)
@@ -749,14 +762,14 @@ int create_plan(pkv_plan **out, const pkv_plan_desc *desc, const pkv_plan_caps *
 int pkv_plan_create(pkv_plan **out, const pkv_plan_desc *desc, void *stream)
 {
     NvtxRange range("pkv_plan_create");
-    return create_plan(out, desc, nullptr, 0, stream);
+    return guarded([&] { return create_plan(out, desc, nullptr, 0, stream); });
 }
 
 int pkv_plan_create_sinks(pkv_plan **out, const pkv_plan_desc *desc, int32_t num_sinks, const pkv_plan_caps *caps,
                           void *stream)
 {
     NvtxRange range("pkv_plan_create_sinks");
-    return create_plan(out, desc, caps, num_sinks, stream);
+    return guarded([&] { return create_plan(out, desc, caps, num_sinks, stream); });
 }
 
 int pkv_plan_create_capturable(pkv_plan **out, const pkv_plan_desc *desc, const pkv_plan_caps *caps,
@@ -769,13 +782,11 @@ int pkv_plan_create_capturable(pkv_plan **out, const pkv_plan_desc *desc, const 
             *out = nullptr;
         return fail(PKV_ERR_INVALID_ARG, "caps is NULL");
     }
-    return create_plan(out, desc, caps, 0, stream);
+    return guarded([&] { return create_plan(out, desc, caps, 0, stream); });
 }
 
-int pkv_plan_update(pkv_plan *plan, const pkv_plan_desc *desc, void *stream_)
+static int update_plan(pkv_plan *plan, const pkv_plan_desc *desc, void *stream_)
 {
-    NvtxRange range("pkv_plan_update");
-    g_last_error.clear();
     if (!plan)
         return fail(PKV_ERR_INVALID_ARG, "plan is NULL");
     if (!plan->capturable)
@@ -836,6 +847,13 @@ int pkv_plan_update(pkv_plan *plan, const pkv_plan_desc *desc, void *stream_)
     plan->desc.fixed_split_size = d.fixed_split_size;
     plan->desc.disable_split_kv = d.disable_split_kv;
     return PKV_OK;
+}
+
+int pkv_plan_update(pkv_plan *plan, const pkv_plan_desc *desc, void *stream)
+{
+    NvtxRange range("pkv_plan_update");
+    g_last_error.clear();
+    return guarded([&] { return update_plan(plan, desc, stream); });
 }
 
 int pkv_plan_destroy(pkv_plan *plan)

@@ -272,3 +272,24 @@ def test_bad_page_ids_are_recorded(pkv):
             plan = pkv.plan_for(wd, num_sinks=4)
             plan.run(wd.q, wd.k_cache, wd.v_cache)
             assert plan.device_status() == pkv.PKV_ERR_DEVICE_BOUNDS
+
+
+def test_invisible_keys_of_a_prefill_may_hold_anything_in_k(pkv, oracle_lib):
+    """NaN in K wherever no query looks (V finite in the request's own keys), and NaN in both
+    in pages of nobody: the same bits as with a clean cache."""
+    for P in (1, 16, 64):
+        W, sinks, qo, kv = 30, 5, [40, 130, 1], [300, 700, 90]
+        w = _workload("prefill", 59, qo, kv, W, P=P)
+        clean = _run(pkv, w, sinks)
+        seen, own = (torch.zeros(w.num_pages, P, dtype=torch.bool) for _ in range(2))
+        for b in range(3):
+            for j in range(kv[b]):
+                at = int(w.kv_indices[int(w.kv_indptr[b]) + j // P]), j % P
+                own[at] = True
+                seen[at] = j < sinks or j >= kv[b] - qo[b] - W
+        k, v = w.k_cache.clone(), w.v_cache.clone()
+        k[~seen] = float("nan")
+        v[~own] = float("nan")
+        dirty = _run(pkv, replace(w, k_cache=k, v_cache=v), sinks)
+        assert torch.equal(clean[0], dirty[0]) and torch.equal(clean[1], dirty[1]), P
+        _check(oracle_lib, w, clean[0], clean[1], sinks, f"P {P}")

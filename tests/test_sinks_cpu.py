@@ -3,7 +3,6 @@ float64 and against its limits, and what the plan refuses on the host."""
 from __future__ import annotations
 
 import ctypes
-import math
 
 import numpy as np
 import pytest
@@ -70,4 +69,3 @@ def test_plan_refuses_bad_sinks_on_the_host():
     caps.max_batch, caps.max_total_q = 1, 100  # below the batch of 2
     assert lib.pkv_plan_create_sinks(ctypes.byref(h), ctypes.byref(d), 4, ctypes.byref(caps),
                                      None) == pkv.PKV_ERR_INVALID_ARG
-    assert math.isfinite(d.sm_scale)

@@ -452,7 +452,8 @@ PKV_API int pkv_pages_workspace(int32_t num_rows, int32_t num_pages, int64_t *by
  * return PKV_OK, PKV_ERR_INVALID_ARG, PKV_ERR_UNSUPPORTED (sizes near 2^31) or PKV_ERR_CUDA.
  *
  * pkv_pages_extend: rows[i] grows by add[i] tokens. slots (or NULL) gets, entry after
- * entry, each new token's slot page * page_size + offset, slots_capacity at most.
+ * entry, each new token's slot page * page_size + offset, and -1 from there to
+ * slots_capacity, so that an append captured for that many rows passes over the rest.
  */
 PKV_API int pkv_pages_extend(const pkv_page_pool *pool, const int32_t *rows, const int32_t *add, int32_t n,
                              int64_t *slots, int64_t slots_capacity, void *stream);

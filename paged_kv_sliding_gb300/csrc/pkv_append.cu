@@ -333,13 +333,13 @@ extern "C" PKV_API int pkv_norm_rope_append(const pkv_append_desc *desc, const v
             return refuse(PKV_ERR_INVALID_ARG, "weight_offset, k_scale and v_scale must be finite");
     if (!(d.eps >= 0.f) || !std::isfinite(d.eps))
         return refuse(PKV_ERR_INVALID_ARG, "eps must be finite and not negative");
+    if (d.num_tokens == 0)
+        return PKV_OK;
     const bool cache = k_cache || v_cache;
     if (cache && (!k_cache || !v_cache || !slots || d.num_kv_heads == 0))
         return refuse(PKV_ERR_INVALID_ARG, "k_cache, v_cache, slots and KV heads come together");
     if (cache && (d.page_size <= 0 || d.num_pages < 0))
         return refuse(PKV_ERR_INVALID_ARG, "page_size or num_pages");
-    if (d.num_tokens == 0)
-        return PKV_OK;
     if (d.num_qo_heads > 0 && (!q || !q_out))
         return refuse(PKV_ERR_INVALID_ARG, "q and q_out are required");
     if (d.num_kv_heads > 0 && (!k || (!k_out && !cache) || (cache && !v)))

@@ -54,6 +54,7 @@ struct PoolParams {
                          // which a child's may replace when a row is both)
     int32_t *free_ids;   // [num_pages] the free pages by rank (compact: a page's rank)
     int32_t *word;       // extend, fork: what does not fit; compact: the live pages
+    int64_t *tokens;     // extend: the call's new tokens
 };
 
 __device__ __forceinline__ int ceil_div(int64_t x, int p) { return (int)((x + p - 1) / p); }
@@ -307,6 +308,8 @@ __global__ void __launch_bounds__(kThreads) rank_kernel(const PoolParams p, cons
         page_at += __shfl_sync(0xffffffffu, before + need, 31);
         token_at += __shfl_sync(0xffffffffu, t_before + t, 31);
     }
+    if (gw == 0 && lane == 0)
+        *p.tokens = all_tokens;
     if (bad || (OP == kExtend && slots && all_tokens > slots_capacity))
         atomicOr(p.word, kBad);
     if (gw == 0 && lane == 0 && want > there)
@@ -330,13 +333,13 @@ __global__ void __launch_bounds__(kApplyThreads) extend_kernel(const PoolParams 
     grid_dependency_wait();
     grid_launch_dependents();
     const int i = blockIdx.x, P = p.page_size;
-    if (!granted(p)) {
-        if (slots)  // no slot: the calls that take them skip it
-            for (int64_t k = (int64_t)i * kApplyThreads + threadIdx.x; k < slots_capacity;
-                 k += (int64_t)gridDim.x * kApplyThreads)
-                slots[k] = -1;
+    const bool done = granted(p);
+    if (slots)  // behind the call's tokens no slot: the calls that take them skip it
+        for (int64_t k = (done ? *p.tokens : 0) + (int64_t)i * kApplyThreads + threadIdx.x; k < slots_capacity;
+             k += (int64_t)gridDim.x * kApplyThreads)
+            slots[k] = -1;
+    if (!done)
         return;
-    }
     const int row = rows[i], len = p.lens[row], more = add[i];
     const int have = ceil_div(len, P), upto = ceil_div((int64_t)len + more, P);
     int32_t *entries = p.table + row * p.row_stride;
@@ -645,7 +648,7 @@ bool misaligned(const void *p, uintptr_t a) { return (uintptr_t)p % a != 0; }
 int64_t align256(int64_t x) { return (x + 255) / 256 * 256; }
 
 struct Carve {
-    int64_t claim, first, first_slot, free_ids, word, bytes;
+    int64_t claim, first, first_slot, free_ids, word, tokens, bytes;
 };
 
 Carve carve(int32_t num_rows, int32_t num_pages)
@@ -656,6 +659,7 @@ Carve carve(int32_t num_rows, int32_t num_pages)
     c.first_slot = align256(c.first + 4LL * num_rows);
     c.free_ids = align256(c.first_slot + 8LL * num_rows);
     c.word = align256(c.free_ids + 4LL * num_pages);
+    c.tokens = c.word + 8;
     c.bytes = c.word + 256;
     return c;
 }
@@ -693,6 +697,7 @@ int take_pool(const char *call, const pkv_page_pool *pool, PoolParams &p)
     p.first_slot = (int64_t *)(w + c.first_slot);
     p.free_ids = (int32_t *)(w + c.free_ids);
     p.word = (int32_t *)(w + c.word);
+    p.tokens = (int64_t *)(w + c.tokens);
     return PKV_OK;
 }
 
@@ -760,8 +765,11 @@ PKV_API int pkv_pages_extend(const pkv_page_pool *pool, const int32_t *rows, con
         return st;
     if (slots_capacity < 0 || misaligned(slots, 8))
         return refuse(PKV_ERR_INVALID_ARG, "pkv_pages_extend", "slots are misaligned or their capacity negative");
-    if (n == 0)
-        return PKV_OK;
+    if (n == 0)  // -1 in every slot
+        return slots && slots_capacity > 0
+                   ? launched("pkv_pages_extend",
+                              cudaMemsetAsync(slots, 0xff, slots_capacity * sizeof(int64_t), (cudaStream_t)stream))
+                   : PKV_OK;
     cudaError_t ce = launch(rank_kernel<kExtend>, kCtas, kThreads, kCtas, stream, p, rows, add, (int)n, slots != nullptr,
                             slots_capacity);
     if (ce == cudaSuccess)

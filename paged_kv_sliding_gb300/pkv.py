@@ -228,6 +228,13 @@ def _stream_handle(stream=None) -> int:
     return int(stream.cuda_stream)
 
 
+def _on(stream, *tensors):
+    """The tensors, which were allocated on the current stream, are used on `stream`."""
+    if stream is not None:
+        for t in tensors:
+            t.record_stream(stream)
+
+
 def _ptrs(*tensors):
     return [None if t is None else t.data_ptr() for t in tensors]
 
@@ -532,6 +539,7 @@ def norm_rope_append(q: Optional[torch.Tensor], k: Optional[torch.Tensor], v: Op
     lib = _lib or load_library()
     if q is not None and q_out is None:
         q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+        _on(stream, q_out)
     dev = torch.cuda.current_device()
     tensors = (q, k, v, q_weight, k_weight, cos_sin, positions, slots, q_out, k_out, k_cache, v_cache, status)
     key = (dev, eps, weight_offset, interleaved, k_scale, v_scale) + tuple(map(_sig, tensors))
@@ -593,6 +601,7 @@ class PagePool:
         n = self._index(rows, add)
         if slots is None and total is not None:
             slots = torch.empty(total, dtype=torch.int64, device=self.table.device)
+            _on(stream, slots)
         elif slots is not None:
             _want(slots, "slots", torch.int64)
         _check(self._lib.pkv_pages_extend(self._desc, rows.data_ptr(), add.data_ptr(), n,
@@ -607,6 +616,7 @@ class PagePool:
         partly filled last one is new. Returns (src, dst), the pages to copy (or -1)."""
         src = torch.empty_like(parents) if src is None else src
         dst = torch.empty_like(parents) if dst is None else dst
+        _on(stream, src, dst)
         n = self._index(parents, children, src, dst)
         _check(self._lib.pkv_pages_fork(self._desc, parents.data_ptr(), children.data_ptr(), n, src.data_ptr(),
                                         dst.data_ptr(), _stream_handle(stream)), "pkv_pages_fork")
@@ -629,6 +639,7 @@ class PagePool:
             dst = torch.empty_like(src)
         if count is None:
             count = torch.empty(1, dtype=torch.int32, device=self.table.device)
+        _on(stream, src, dst, count)
         n = self._index(src, dst)
         self._index(count)
         _check(self._lib.pkv_pages_compact(self._desc, (out or self)._desc, src.data_ptr(), dst.data_ptr(), n,

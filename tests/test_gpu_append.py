@@ -177,6 +177,44 @@ def test_parts_alone_and_in_place(pkv):
     assert torch.equal(q, q_out) and torch.equal(k, k_out)
 
 
+def test_no_tokens_and_padding_without_a_cache(pkv):
+    s = _inputs(20, 4, 2, 128, 16, 128, "bf16", seed=10, pad=(2, 19))
+    args = dict(cos_sin=s["cos_sin"], q_weight=s["wq"], k_weight=s["wk"])
+    got = pkv.norm_rope_append(s["q"][:0], s["k"][:0], s["v"][:0], positions=s["positions"][:0], slots=s["slots"][:0],
+                               k_cache=s["k_cache"], v_cache=s["v_cache"], **args)
+    assert got.shape == (0, 4, 128)
+    k_out = torch.full((20, 2, 128), 9.0, dtype=torch.bfloat16, device="cuda")
+    q_out = torch.full((20, 4, 128), 9.0, dtype=torch.bfloat16, device="cuda")
+    pkv.norm_rope_append(s["q"], s["k"], positions=s["positions"], slots=s["slots"], k_out=k_out, q_out=q_out, **args)
+    skipped = (k_out == 9.0).all(-1).all(-1).nonzero().flatten().tolist()
+    assert skipped == [2, 19] == (q_out == 9.0).all(-1).all(-1).nonzero().flatten().tolist()
+
+
+def test_one_row_for_every_token(pkv):
+    """A token stride of zero: the same row at every position."""
+    s = _inputs(30, 4, 2, 128, 16, 128, "bf16", seed=11)
+    q = s["q"][:1].contiguous()
+    args = dict(positions=s["positions"], cos_sin=s["cos_sin"], q_weight=s["wq"])
+    assert torch.equal(pkv.norm_rope_append(q.expand(30, -1, -1), None, **args),
+                       pkv.norm_rope_append(q.expand(30, -1, -1).contiguous(), None, **args))
+
+
+def test_v_of_a_bf16_cache_is_v_bit_for_bit(pkv):
+    """Every bf16 there is, zeros of both signs, subnormals and infinities among them."""
+    bits = torch.arange(1 << 16, device="cuda").to(torch.int16)
+    v = bits.view(torch.bfloat16).view(-1, 2, 64)
+    n = v.shape[0]
+    k_cache = torch.zeros(n // 8, 8, 2, 64, dtype=torch.bfloat16, device="cuda")
+    v_cache = torch.zeros_like(k_cache)
+    slots = torch.randperm(n, device="cuda")
+    pkv.norm_rope_append(None, v, v, slots=slots, k_cache=k_cache, v_cache=v_cache)
+    for cache in (k_cache, v_cache):  # k too: neither normalised nor rotated
+        got = cache.view(-1, 2, 64)[slots]
+        assert torch.equal(torch.isnan(got), torch.isnan(v))
+        same = got.view(torch.int16) == v.view(torch.int16)
+        assert (same | torch.isnan(v)).all()
+
+
 def test_bad_slots_and_positions_are_recorded(pkv):
     for name, value in (("slots", 10 ** 9), ("slots", 1 << 40), ("positions", 500), ("positions", -1)):
         s = _inputs(20, 4, 2, 128, 16, 128, "bf16", seed=6)

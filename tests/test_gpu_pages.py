@@ -140,7 +140,11 @@ def test_slots_beyond_their_capacity_are_refused(pkv):
     slots = torch.full((7,), 77, dtype=torch.int64, device="cuda")
     model, out = _both(lambda: pool.extend(_dev([0, 1]), _dev([2, 3]), slots=slots), lambda: model.extend([0, 1], [2, 3]),
                        pool, model, "room")
-    assert slots.cpu().tolist() == out[0] + [77, 77]  # behind the last one: left as it was
+    assert slots.cpu().tolist() == out[0] + [-1, -1]  # behind the last one: no slot
+    nobody = _dev([])
+    pool.extend(nobody, nobody, slots=slots)
+    assert (slots == -1).all() and pool.device_status() == 0
+    _same(pool, model)
 
 
 @pytest.mark.parametrize("parents,children", [([0], [3]), ([0, 0], [1, 1]), ([9], [1]), ([0], [-3]), ([0], [0])])
@@ -332,9 +336,39 @@ def test_captured_and_replayed(pkv):
         model, a, z = model.fork(parents.tolist(), children.tolist())
         assert pool.device_status() == 0
         _same(pool, model, str(more))
-        assert slots[: len(want)].cpu().tolist() == want and src.cpu().tolist() == a and dst.cpu().tolist() == z
+        assert slots.cpu().tolist() == want + [-1] * (120 - len(want)) and src.cpu().tolist() == a and dst.cpu().tolist() == z
         for x, y in zip(a, z):
             assert x < 0 or (torch.equal(k[x], k[y]) and torch.equal(v[x], v[y]))
+
+
+def test_another_stream(pkv):
+    """The calls of a step on a side stream, their outputs allocated by the binding."""
+    pool, model = _pair(pkv, 16, 12, 120, 8)
+    k = torch.randn(120, 8, 1, 64, device="cuda").to(torch.bfloat16)
+    v = k.clone()
+    rows, add, parents, children = (_dev(x) for x in ([0, 1, 2], [20, 7, 33], [0, 2], [8, 9]))
+    q = torch.randn(60, 2, 64, device="cuda").to(torch.bfloat16)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    slots = pool.extend(rows, add, total=60, stream=side)
+    pkv.norm_rope_append(q, q[:, :1], q[:, 1:], slots=slots, k_cache=k, v_cache=v, stream=side)
+    src, dst = pool.fork(parents, children, stream=side)
+    pkv.copy_pages(k, v, src, dst, stream=side)
+    pool.free(rows, stream=side)
+    moves = pool.compact(stream=side)
+    pkv.copy_pages(k, v, *moves[:2], count=moves[2], stream=side)
+    side.synchronize()
+    model, want = model.extend([0, 1, 2], [20, 7, 33])
+    model, a, z = model.fork([0, 2], [8, 9])
+    assert slots.cpu().tolist() == want and src.cpu().tolist() == a and dst.cpu().tolist() == z
+    model, a, z = model.free([0, 1, 2]).compact()
+    assert pool.device_status() == 0 and moves[2].item() == len(a)
+    _same(pool, model)
+    for row, first in ((8, 0), (9, 27)):  # the forks hold their parents' tokens
+        n = int(model.lens[row])
+        at = [int(model.table[row, t // 8]) * 8 + t % 8 for t in range(n)]
+        assert torch.equal(k.view(-1, 1, 64)[at], q[first: first + n, :1])
+        assert torch.equal(v.view(-1, 1, 64)[at], q[first: first + n, 1:])
 
 
 def test_refusals_of_the_binding(pkv):

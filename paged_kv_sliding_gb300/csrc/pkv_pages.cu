@@ -24,6 +24,7 @@
 #include <cooperative_groups.h>
 
 #include <string>
+#include <utility>
 
 #include "pkv_internal.h"
 #include "pkv_nvtx.h"
@@ -57,17 +58,15 @@ struct PoolParams {
     int64_t *tokens;     // extend: the call's new tokens
 };
 
-__device__ __forceinline__ int ceil_div(int64_t x, int p) { return (int)((x + p - 1) / p); }
+// ceil(x / p) for 0 <= x < 2^31.
+__device__ __forceinline__ int ceil_div(int64_t x, int p) { return (int)(((unsigned)x + (unsigned)p - 1u) / (unsigned)p); }
 
-// What the CTAs of a cluster tell one another.
+// What every warp of the cluster counted, in each CTA's shared memory: new pages, free
+// pages and new tokens of its segment.
 struct Board {
-    int32_t pages[kWarps];   // by warp: new pages, free pages, new tokens of its segment
-    int32_t frees[kWarps];
-    long long tokens[kWarps];
-    // every warp's, after the exchange
-    int32_t all_pages[kAllWarps];
-    int32_t all_frees[kAllWarps];
-    long long all_tokens[kAllWarps];
+    uint32_t pages[kAllWarps];
+    uint32_t frees[kAllWarps];
+    long long tokens[kAllWarps];
 };
 
 // Neighbouring segments go to different CTAs: the lowest free pages, which a call wants, lie
@@ -77,7 +76,7 @@ __device__ __forceinline__ int warp_of_cluster(const cg::cluster_group &cluster,
     return warp * kCtas + (int)cluster.block_rank();
 }
 
-__device__ __forceinline__ int32_t warp_sum(int32_t x) { return __reduce_add_sync(0xffffffffu, x); }
+__device__ __forceinline__ uint32_t warp_sum(uint32_t x) { return __reduce_add_sync(0xffffffffu, x); }
 
 __device__ __forceinline__ long long warp_sum64(long long x)
 {
@@ -152,7 +151,7 @@ __device__ int segment_free(const int32_t *refs, int lo, int hi, int lane)
     }
     for (int p = base + 4 * lane; p < hi; p += 128)
         n += count_free(refs4(refs, p, hi));
-    return warp_sum(n);
+    return (int)warp_sum((uint32_t)n);
 }
 
 // The ids of the free pages of [lo, hi), the first of which has rank `rank`, into
@@ -167,8 +166,10 @@ __device__ void write_free(const PoolParams &p, int lo, int hi, int rank, int wa
 #pragma unroll
         for (int u = 0; u < kDeep; ++u) {
             const int at = base + 128 * u + 4 * lane;
-            const int n = count_free(r[u]), before = warp_before(n, lane);
-            int k = rank + before;
+            const uint32_t m0 = __ballot_sync(0xffffffffu, r[u].x == 0), m1 = __ballot_sync(0xffffffffu, r[u].y == 0);
+            const uint32_t m2 = __ballot_sync(0xffffffffu, r[u].z == 0), m3 = __ballot_sync(0xffffffffu, r[u].w == 0);
+            const uint32_t lower = (1u << lane) - 1u;
+            int k = rank + __popc(m0 & lower) + __popc(m1 & lower) + __popc(m2 & lower) + __popc(m3 & lower);
             if (r[u].x == 0 && k < want)
                 p.free_ids[k] = at;
             k += r[u].x == 0;
@@ -180,28 +181,46 @@ __device__ void write_free(const PoolParams &p, int lo, int hi, int rank, int wa
             k += r[u].z == 0;
             if (r[u].w == 0 && k < want)
                 p.free_ids[k] = at + 3;
-            rank += __shfl_sync(0xffffffffu, before + n, 31);
+            rank += __popc(m0) + __popc(m1) + __popc(m2) + __popc(m3);
         }
     }
 }
 
-// Collect every warp's counts in each CTA (behind a cluster barrier).
-__device__ void exchange(cg::cluster_group &cluster, Board &b)
+// Tell every CTA of the cluster what this warp counted (8 lanes, a CTA each; the CTAs have
+// all started: the caller waited for it), and wait for the others. Afterwards the board is
+// only read where it lies, so that a CTA may leave when it likes.
+__device__ void exchange(cg::cluster_group &cluster, Board &b, int gw, int lane, uint32_t pages, uint32_t frees,
+                         long long tokens)
 {
-    cluster.sync();
-    if (threadIdx.x < kAllWarps) {
-        const Board *from = cluster.map_shared_rank(&b, threadIdx.x % kCtas);
-        const int w = threadIdx.x / kCtas;
-        b.all_pages[threadIdx.x] = from->pages[w];
-        b.all_frees[threadIdx.x] = from->frees[w];
-        b.all_tokens[threadIdx.x] = from->tokens[w];
+    if (lane < kCtas) {
+        Board *to = cluster.map_shared_rank(&b, lane);
+        to->pages[gw] = pages;
+        to->frees[gw] = frees;
+        to->tokens[gw] = tokens;
     }
-    __syncthreads();
+    cluster.sync();
 }
 
-// Sum over the warps before gw, and over all, of one of the boards' arrays.
-template <typename T>
-__device__ __forceinline__ void before_and_total(const T *all, int gw, int lane, long long &before, long long &total)
+// Sum over the warps before gw, and over all, of one of the board's arrays (32-bit counts:
+// as halves, whose sums stay below 2^32).
+__device__ __forceinline__ void before_and_total(const uint32_t *all, int gw, int lane, long long &before, long long &total)
+{
+    uint32_t s_lo = 0, s_hi = 0, t_lo = 0, t_hi = 0;
+#pragma unroll
+    for (int k = 0; k < kAllWarps / 32; ++k) {
+        const uint32_t v = all[32 * k + lane], lo = v & 0xffffu, hi = v >> 16;
+        const bool mine = 32 * k + lane < gw;
+        t_lo += lo;
+        t_hi += hi;
+        s_lo += mine ? lo : 0;
+        s_hi += mine ? hi : 0;
+    }
+    before = warp_sum(s_lo) + ((long long)warp_sum(s_hi) << 16);
+    total = warp_sum(t_lo) + ((long long)warp_sum(t_hi) << 16);
+}
+
+__device__ __forceinline__ void before_and_total(const long long *all, int gw, int lane, long long &before,
+                                                 long long &total)
 {
     long long s = 0, t = 0;
 #pragma unroll
@@ -229,6 +248,7 @@ __global__ void __launch_bounds__(kThreads) rank_kernel(const PoolParams p, cons
 {
     __shared__ Board b;
     cg::cluster_group cluster = cg::this_cluster();
+    auto started = cluster.barrier_arrive();
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, gw = warp_of_cluster(cluster, warp);
     const int P = p.page_size;
     grid_dependency_wait();
@@ -236,85 +256,94 @@ __global__ void __launch_bounds__(kThreads) rank_kernel(const PoolParams p, cons
     if (gw == 0 && lane == 0)
         *p.word = 0;
 
-    // What each entry of the warp's segment needs, and the free pages of its segment.
+    // What each entry of the warp's segment needs, and the free pages of its segment. The
+    // first 32 entries (nearly always all) stay in registers for the second pass.
     int e_lo, e_hi, p_lo, p_hi;
     segment(n, 1, gw, e_lo, e_hi);
     segment(p.num_pages, 4, gw, p_lo, p_hi);
-    const int frees = segment_free(p.refs, p_lo, p_hi, lane);
-    auto need_of = [&](int i, long long &tokens) -> int {
-        tokens = 0;
-        if (i >= e_hi)
-            return 0;
-        const int row = rows[i];
-        if ((unsigned)row >= (unsigned)p.num_rows)
-            return -1;
-        const int64_t len = p.lens[row];
-        if (OP == kExtend) {
-            tokens = add[i];
-            if (tokens < 0 || !len_fine(p, len) || len + tokens > INT32_MAX || !len_fine(p, len + tokens)) {
-                tokens = 0;
-                return -1;
-            }
-            return ceil_div(len + tokens, P) - ceil_div(len, P);
-        }
-        const int parent = add[i];
-        if ((unsigned)parent >= (unsigned)p.num_rows || len != 0)
-            return -1;
-        tokens = p.lens[parent];
-        return len_fine(p, tokens) ? tokens % P != 0 : -1;
+    struct Entry {
+        int row, more;  // more: add, or the parent
+        int need;       // new pages; -1: does not fit
+        long long tokens;
     };
+    auto index = [&](int i) -> Entry { return {i < e_hi ? rows[i] : -1, i < e_hi ? add[i] : 0, 0, 0}; };
+    auto measure = [&](int i, Entry &e) {
+        if (i >= e_hi)
+            return;
+        e.need = -1;
+        if ((unsigned)e.row >= (unsigned)p.num_rows)
+            return;
+        const int64_t len = p.lens[e.row];
+        if (OP == kExtend) {
+            if (e.more < 0 || !len_fine(p, len) || len + e.more > INT32_MAX || !len_fine(p, len + e.more))
+                return;
+            e.tokens = e.more;
+            e.need = ceil_div(len + e.more, P) - ceil_div(len, P);
+        } else {
+            if ((unsigned)e.more >= (unsigned)p.num_rows || len != 0)
+                return;
+            e.tokens = p.lens[e.more];
+            e.need = !len_fine(p, e.tokens) ? -1 : (int)((unsigned)e.tokens % (unsigned)P != 0);
+        }
+    };
+    Entry first = index(e_lo + lane);
+    const int frees = segment_free(p.refs, p_lo, p_hi, lane);
     long long pages = 0, tokens = 0;
     bool bad = false;
     for (int i0 = e_lo; i0 < e_hi; i0 += 32) {
         const int i = i0 + lane;
-        long long t;
-        const int need = need_of(i, t);
-        if (need < 0)
+        Entry e = i0 == e_lo ? first : index(i);
+        measure(i, e);
+        if (e.need < 0)
             bad = true;
         else if (i < e_hi)
-            p.claim[rows[i]] = i;
-        pages += max(need, 0);
-        tokens += t;
+            p.claim[e.row] = i;
+        pages += max(e.need, 0);
+        tokens += e.tokens;
+        if (i0 == e_lo)
+            first = e;
     }
     pages = warp_sum64(pages);
     tokens = warp_sum64(tokens);
-    if (lane == 0) {
-        b.pages[warp] = (int32_t)min(pages, p.num_pages + 1LL);  // more than there are: too many in any case
-        b.frees[warp] = frees;
-        b.tokens[warp] = tokens;
-    }
-    exchange(cluster, b);
+    cluster.barrier_wait(std::move(started));
+    // (more pages than there are: too many in any case)
+    exchange(cluster, b, gw, lane, (uint32_t)min(pages, p.num_pages + 1LL), (uint32_t)frees, tokens);
 
     // Ranks: an entry's first new page and slot, the ids of the free pages that are wanted.
-    long long page_at, want, rank, there, token_at, all_tokens;
-    before_and_total(b.all_pages, gw, lane, page_at, want);
-    before_and_total(b.all_frees, gw, lane, rank, there);
-    before_and_total(b.all_tokens, gw, lane, token_at, all_tokens);
+    int claimed = e_lo + lane < e_hi && (unsigned)first.row < (unsigned)p.num_rows ? __ldcg(p.claim + first.row) : 0;
+    long long page_at, want, rank, there, token_at = 0, all_tokens = 0;
+    before_and_total(b.pages, gw, lane, page_at, want);
+    before_and_total(b.frees, gw, lane, rank, there);
+    if (OP == kExtend)
+        before_and_total(b.tokens, gw, lane, token_at, all_tokens);
     if (want <= there)
         write_free(p, p_lo, p_hi, (int)rank, (int)want, lane);
     for (int i0 = e_lo; i0 < e_hi; i0 += 32) {
         const int i = i0 + lane;
-        long long t;
-        const int need = max(need_of(i, t), 0);
-        const int before = warp_before(need, lane);
-        const long long t_before = warp_before64(t, lane);
+        Entry e = first;
+        if (i0 != e_lo) {
+            e = index(i);
+            measure(i, e);
+            claimed = i < e_hi && (unsigned)e.row < (unsigned)p.num_rows ? __ldcg(p.claim + e.row) : 0;
+        }
+        const int need = max(e.need, 0), before = warp_before(need, lane);
+        const long long t_before = OP == kExtend ? warp_before64(e.tokens, lane) : 0;
         if (i < e_hi) {
             p.first[i] = (int32_t)(page_at + before);
-            p.first_slot[i] = OP == kExtend ? token_at + t_before : t;
-            const int row = rows[i];
-            if ((unsigned)row < (unsigned)p.num_rows && __ldcg(p.claim + row) != i)
+            p.first_slot[i] = OP == kExtend ? token_at + t_before : e.tokens;
+            if ((unsigned)e.row < (unsigned)p.num_rows && claimed != i)
                 bad = true;  // another entry names the row too
         }
         page_at += __shfl_sync(0xffffffffu, before + need, 31);
-        token_at += __shfl_sync(0xffffffffu, t_before + t, 31);
+        token_at += __shfl_sync(0xffffffffu, t_before + e.tokens, 31);
     }
-    if (gw == 0 && lane == 0)
+    if (gw == 0 && lane == 0) {
         *p.tokens = all_tokens;
+        if (want > there)
+            atomicOr(p.word, kTooMany);
+    }
     if (bad || (OP == kExtend && slots && all_tokens > slots_capacity))
         atomicOr(p.word, kBad);
-    if (gw == 0 && lane == 0 && want > there)
-        atomicOr(p.word, kTooMany);
-    cluster.sync();  // no CTA leaves while another reads its board
 }
 
 // Whether the ranked call can be done; if not, block 0 records why.
@@ -452,21 +481,18 @@ __global__ void __launch_bounds__(kThreads) moves_kernel(const PoolParams p, int
     __shared__ Board b;
     __shared__ int edge_live;  // live pages below n_live in the segment that n_live falls into
     cg::cluster_group cluster = cg::this_cluster();
+    auto started = cluster.barrier_arrive();
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, gw = warp_of_cluster(cluster, warp);
     grid_dependency_wait();
     grid_launch_dependents();
     int lo, hi;
     segment(p.num_pages, 4, gw, lo, hi);
     const int frees = segment_free(p.refs, lo, hi, lane);
-    if (lane == 0) {
-        b.pages[warp] = hi - lo - frees;  // live
-        b.frees[warp] = frees;
-        b.tokens[warp] = 0;
-    }
-    exchange(cluster, b);
+    cluster.barrier_wait(std::move(started));
+    exchange(cluster, b, gw, lane, (uint32_t)(hi - lo - frees), (uint32_t)frees, 0);  // pages: the live ones
     long long live_before, n_live, free_before, n_free;
-    before_and_total(b.all_pages, gw, lane, live_before, n_live);
-    before_and_total(b.all_frees, gw, lane, free_before, n_free);
+    before_and_total(b.pages, gw, lane, live_before, n_live);
+    before_and_total(b.frees, gw, lane, free_before, n_free);
     // The holes are the free pages below n_live: a warp's first has rank free_before. The
     // movers are the live pages from n_live on: rank = live pages before it minus those
     // below n_live, n_live - holes.
@@ -482,7 +508,7 @@ __global__ void __launch_bounds__(kThreads) moves_kernel(const PoolParams p, int
     }
     __syncthreads();
     long long edge_before, unused;
-    before_and_total(b.all_pages, edge, lane, edge_before, unused);
+    before_and_total(b.pages, edge, lane, edge_before, unused);
     const int live_below = (int)edge_before + edge_live;
     const int moves = N - live_below;  // as many movers as holes
     const bool fits = moves <= max_moves;
@@ -544,7 +570,6 @@ __global__ void __launch_bounds__(kThreads) moves_kernel(const PoolParams p, int
         if (!fits)
             record_status(p.status, PKV_ERR_DEVICE_BOUNDS);
     }
-    cluster.sync();
 }
 
 // Table entries by the moves: one CTA a row.

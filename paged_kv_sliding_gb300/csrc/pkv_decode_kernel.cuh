@@ -770,14 +770,10 @@ cudaError_t launch_decode_dt(const DecodeParams &p, const CUtensorMap &tk, const
                              cudaStream_t s, bool overlap_prev)
 {
     using Tr = DecTraits<D, TT, KV, TPW>;
-    static bool configured = false;
-    if (!configured) {
-        cudaError_t e = cudaFuncSetAttribute(decode_kernel<D, TMA_KV, TT, KV, TPW, SINK>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, Tr::kDynSmem);
-        if (e != cudaSuccess)
-            return e;
-        configured = true;
-    }
+    static std::atomic<uint64_t> configured{0};
+    const cudaError_t e = allow_smem(decode_kernel<D, TMA_KV, TT, KV, TPW, SINK>, Tr::kDynSmem, configured);
+    if (e != cudaSuccess)
+        return e;
     // Programmatic stream serialisation (overlap_prev): this grid's set-up (barriers,
     // work item) may overlap the tail of the previous kernel in the stream; the kernel
     // waits for that kernel's completion before it touches q, the caches or the page

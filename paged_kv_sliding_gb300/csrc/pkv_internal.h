@@ -2,6 +2,7 @@
 // Not part of the C ABI (include/pkv.h is).
 #pragma once
 
+#include <atomic>
 #include <cstdint>
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -261,6 +262,21 @@ cudaError_t launch_prefill_pp_sinks(const PrefillParams &p, int head_dim, int ma
                                     const CUtensorMap &to, int num_ctas, cudaStream_t s);
 cudaError_t launch_prefill_pp_kv8_sinks(const PrefillParams &p, int head_dim, int mask_mode, int num_ctas,
                                         cudaStream_t s);
+
+// Allow `kernel` its dynamic shared memory on the current device; `done` holds the devices
+// (a bit each) on which that was said before, by any thread.
+template <typename K>
+cudaError_t allow_smem(K kernel, int bytes, std::atomic<uint64_t> &done)
+{
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || (dev < 64 && (done.load(std::memory_order_relaxed) >> dev & 1)))
+        return e;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess && dev < 64)
+        done.fetch_or(1ull << dev, std::memory_order_relaxed);
+    return e;
+}
 
 // Set the calling thread's pkv_last_error() text.
 void set_last_error(const char *msg);

@@ -1335,14 +1335,10 @@ cudaError_t launch_pp_dmt(const PrefillParams &p, const CUtensorMap &tq, const C
                           const CUtensorMap &tv, const CUtensorMap &to, int num_ctas, cudaStream_t s)
 {
     using Tr = PPTraits<D, KV != PKV_BF16>;
-    static bool configured = false;
-    if (!configured) {
-        cudaError_t e = cudaFuncSetAttribute(prefill_pp_kernel<D, MASK, TMA_KV, RAGGED, KV>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, Tr::kDynSmem);
-        if (e != cudaSuccess)
-            return e;
-        configured = true;
-    }
+    static std::atomic<uint64_t> configured{0};
+    const cudaError_t e = allow_smem(prefill_pp_kernel<D, MASK, TMA_KV, RAGGED, KV>, Tr::kDynSmem, configured);
+    if (e != cudaSuccess)
+        return e;
     if (MASK == kMaskCausalWindowSinks || MASK == kMaskWindowSinks) {
         cudaLaunchConfig_t cfg{};
         cfg.gridDim = dim3((unsigned)num_ctas);

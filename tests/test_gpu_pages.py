@@ -460,3 +460,76 @@ def test_a_serving_step_end_to_end(pkv, oracle_lib, P, kv_type):
     after = decode(rest, q)
     assert torch.equal(before[0], after[0]) and torch.equal(before[1], after[1])
     decode(rest, append(rest, [1] * 4))
+
+
+def test_a_captured_step_replayed(pkv, oracle_lib):
+    """One decode step in one graph: a token for every row, its key and value appended, the
+    page table rebuilt, and attention under a window with sinks; replayed step after step
+    with only the inputs, the positions and the plan's lengths renewed."""
+    hq, hkv, d, P, W, sinks, B, pages = 8, 2, 128, 16, 30, 5, 12, 400
+    rng = np.random.default_rng(6)
+    k_cache, v_cache = (torch.randn(pages, P, hkv, d, device="cuda").to(torch.bfloat16) for _ in range(2))
+    pool = pkv.PagePool.empty(num_rows=20, max_pages=30, num_pages=pages, page_size=P)
+    rows = _dev(rng.permutation(20)[:B])
+    start = rng.integers(1, 120, size=B)
+    pool.extend(rows, _dev(start))
+    a = torch.arange(400, dtype=torch.float64, device="cuda")[:, None] * 50.0 ** (-torch.arange(0, d, 2, device="cuda") / d)[None]
+    table = torch.cat([a.cos(), a.sin()], 1).float()
+    weight = (torch.rand(d, device="cuda") + 0.5).to(torch.bfloat16)
+    qkv = torch.zeros(B + 3, (hq + 2 * hkv) * d, dtype=torch.bfloat16, device="cuda")  # three padding rows
+    q, k, v = (x.view(B + 3, -1, d) for x in qkv.split([hq * d, hkv * d, hkv * d], 1))
+    positions, slots = torch.zeros(B + 3, dtype=torch.int32, device="cuda"), torch.zeros(B + 3, dtype=torch.int64, device="cuda")
+    ones, zeros = torch.ones_like(rows), torch.zeros_like(rows)
+    q_out = torch.full((B + 3, hq, d), 7.0, dtype=torch.bfloat16, device="cuda")
+    out, lse = torch.zeros(B, hq, d, dtype=torch.bfloat16, device="cuda"), torch.zeros(B, hq, device="cuda")
+    kv_indptr, kv_indices = torch.zeros(B + 1, dtype=torch.int32, device="cuda"), torch.zeros(360, dtype=torch.int32, device="cuda")
+    long_rows = rows.long()
+
+    def host_lens(lens):
+        n = -(-lens // P)
+        return dict(kv_indptr=np.concatenate([[0], np.cumsum(n)]), kv_last_page_len=lens - (n - 1) * P)
+
+    plan = pkv.Plan(kind="decode", **host_lens(start + 1), kv_indices=kv_indices, num_qo_heads=hq, num_kv_heads=hkv,
+                    head_dim=d, page_size=P, num_pages=pages, window_left=W, num_sinks=sinks, capacity={"max_batch": B})
+
+    def step():
+        pool.extend(rows, ones, slots=slots)
+        pkv.norm_rope_append(q, k, v, positions=positions, cos_sin=table, slots=slots, k_cache=k_cache, v_cache=v_cache,
+                             q_weight=weight, k_weight=weight, q_out=q_out)
+        pkv.build_kv_indices(pool.table, rows, zeros, (pool.lens[long_rows] + P - 1) // P, kv_indptr=kv_indptr,
+                             kv_indices=kv_indices)
+        plan.run(q_out[:B], k_cache, v_cache, out, lse)
+
+    def renew(lens):
+        qkv.copy_(torch.randn(qkv.shape, device="cuda"))
+        positions[:B] = _dev(lens)
+        plan.update(**host_lens(lens + 1))
+
+    def check(lens, what):
+        torch.cuda.synchronize()
+        assert plan.device_status() == pool.device_status() == 0
+        assert (q_out[B:] == 7.0).all() and slots[B:].tolist() == [-1] * 3 and pool.lens[long_rows].tolist() == (lens + 1).tolist()
+        at = host_lens(lens + 1)
+        n = int(at["kv_indptr"][-1])
+        assert torch.equal(k_cache.view(-1, hkv, d)[slots[:B]], pkv.norm_rope_append(
+            k[:B].contiguous(), None, positions=positions[:B], cos_sin=table, q_weight=weight))
+        w = Workload(name=what, kind="decode", qo_indptr=np.arange(B + 1, dtype=np.int32),
+                     kv_indptr=at["kv_indptr"].astype(np.int32), kv_indices=kv_indices.cpu().numpy()[:n],
+                     kv_last_page_len=at["kv_last_page_len"].astype(np.int32), num_qo_heads=hq, num_kv_heads=hkv, head_dim=d,
+                     page_size=P, num_pages=pages, window_left=W, causal=True, sm_scale=d ** -0.5, q=q_out[:B].cpu(),
+                     k_cache=k_cache.cpu(), v_cache=v_cache.cpu())
+        check_attention(oracle_lib, w, out, lse, sinks, what)
+
+    lens = start.copy()
+    renew(lens)
+    step()
+    check(lens, "first")
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    for i in range(20):
+        lens = lens + 1
+        renew(lens)
+        g.replay()
+        if i % 5 == 4:
+            check(lens, f"replay {i}")

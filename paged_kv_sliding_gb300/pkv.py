@@ -537,6 +537,10 @@ def norm_rope_append(q: Optional[torch.Tensor], k: Optional[torch.Tensor], v: Op
     None with k_out [n, H_kv, d]. status: device int32 word for out-of-range slots and
     positions."""
     lib = _lib or load_library()
+    # Plain values before the descriptor is looked up: a tensor of one number would be found
+    # by its identity, and with it the value that it had in an earlier call.
+    eps, weight_offset, k_scale, v_scale = float(eps), float(weight_offset), float(k_scale), float(v_scale)
+    interleaved = bool(interleaved)
     if q is not None and q_out is None:
         q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
         _on(stream, q_out)

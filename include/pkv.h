@@ -454,6 +454,7 @@ PKV_API int pkv_pages_workspace(int32_t num_rows, int32_t num_pages, int64_t *by
  * pkv_pages_extend: rows[i] grows by add[i] tokens. slots (or NULL) gets, entry after
  * entry, each new token's slot page * page_size + offset, and -1 from there to
  * slots_capacity, so that an append captured for that many rows passes over the rest.
+ * Tokens that would go on filling a last page whose entry is no page id get -1 (recorded).
  */
 PKV_API int pkv_pages_extend(const pkv_page_pool *pool, const int32_t *rows, const int32_t *add, int32_t n,
                              int64_t *slots, int64_t slots_capacity, void *stream);

@@ -216,6 +216,28 @@ def test_broken_tables_are_recorded(pkv):
         _both(lambda: pool.extend(_dev([3]), _dev([0])), lambda: model.extend([3], [0]), pool, model, "extend")
 
 
+@pytest.mark.parametrize("value", [-1, -2 ** 31, 30, 2 ** 31 - 1])
+def test_extend_records_a_last_page_that_is_none(pkv, value):
+    """Its tokens have no slot (a negative entry would pass for padding, a large one for a
+    slot beyond the caches); those of the row's new pages and of other rows have theirs."""
+    pool, model = _filled(pkv)
+    pool.table[0, 2] = value  # row 0: 9 tokens, one of them in this page of four
+    model, want = model.extend([5, 0, 3], [2, 8, 1])
+    slots = torch.full((13,), 77, dtype=torch.int64, device="cuda")
+    pool.extend(_dev([5, 0, 3]), _dev([2, 8, 1]), slots=slots)
+    assert pool.device_status() == pkv.PKV_ERR_DEVICE_BOUNDS
+    assert slots.cpu().tolist() == want[:2] + [-1] * 3 + want[5:] + [-1] * 2
+    model.table[0, 2] = value  # left as it is
+    _same(pool, model, "extend")
+    pool, _ = _filled(pkv)
+    pool.table[3, 1] = value  # a full page: not met
+    pool.extend(_dev([0, 3]), _dev([0, 5]), slots=slots)
+    assert pool.device_status() == 0 and (slots[:5] >= 0).all()
+    pool.table[0, 2] = value
+    pool.extend(_dev([0]), _dev([0]), slots=slots)  # no token, nothing met
+    assert pool.device_status() == 0 and (slots == -1).all()
+
+
 def test_compact_out_of_place_and_without_room(pkv):
     pool, model = _filled(pkv)
     pool.free(_dev([0, 5]))

@@ -481,9 +481,10 @@ PKV_API int pkv_pages_free(const pkv_page_pool *pool, const int32_t *rows, int32
  * everything. Writes the moves to src and dst (max_moves at most; num_pages / 2 always
  * do), their number to *count (DEVICE), and the new table entries in use, lens and refs
  * to `out`, whose arrays may be the pool's own (sizes equal, row_stride at least as
- * large). More than max_moves moves: PKV_ERR_DEVICE_BOUNDS is recorded, nothing moves,
- * *count is 0. The caller copies the pages (pkv_copy_pages with count) before it uses the
- * new table, and src are free from then on.
+ * large; a length that is none is recorded and handed on). More than max_moves moves:
+ * PKV_ERR_DEVICE_BOUNDS is recorded, nothing moves, *count is 0. The caller copies the
+ * pages (pkv_copy_pages with count) before it uses the new table, and src are free from
+ * then on.
  */
 PKV_API int pkv_pages_compact(const pkv_page_pool *pool, const pkv_page_pool *out, int32_t *src, int32_t *dst,
                               int32_t max_moves, int32_t *count, void *stream);

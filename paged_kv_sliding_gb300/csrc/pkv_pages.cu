@@ -592,6 +592,8 @@ __global__ void __launch_bounds__(kRewriteThreads) rewrite_kernel(const PoolPara
     const int row = blockIdx.x;
     const int n_live = *p.word;
     const int64_t len = p.lens[row];
+    if (threadIdx.x == 0 && lens_out != p.lens)  // a length that is none too: out is as broken as the pool
+        lens_out[row] = (int32_t)len;
     if (!len_fine(p, len)) {
         if (threadIdx.x == 0)
             record_status(p.status, PKV_ERR_DEVICE_BOUNDS);
@@ -613,8 +615,6 @@ __global__ void __launch_bounds__(kRewriteThreads) rewrite_kernel(const PoolPara
         }
         to[k] = page;
     }
-    if (threadIdx.x == 0 && lens_out != p.lens)
-        lens_out[row] = (int32_t)len;
 }
 
 // Whole pages of K and V, of every layer, in 16-byte granules: a CTA takes tiles of

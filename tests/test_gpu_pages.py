@@ -263,6 +263,21 @@ def test_compact_out_of_place_and_without_room(pkv):
     assert pool.device_status() == pkv.PKV_ERR_DEVICE_BOUNDS and out2[2].item() == 0
 
 
+@pytest.mark.parametrize("length", [25, -3])
+def test_compact_out_of_place_hands_on_a_length_that_is_none(pkv, length):
+    """More than a row's six pages, and a negative one: recorded, and in the new pool what it
+    was in the old, not what that memory held."""
+    pool, model = _filled(pkv)
+    pool.lens[3] = length
+    out = pkv.PagePool(torch.full((8, 7), 55, dtype=torch.int32, device="cuda"), _dev(np.full(8, 1)), _dev(np.full(30, 9)),
+                       page_size=4)
+    pool.compact(out=out)
+    assert pool.device_status() == pkv.PKV_ERR_DEVICE_BOUNDS
+    assert torch.equal(out.lens, pool.lens) and (out.table[3] == 55).all() and torch.equal(out.refs, pool.refs)
+    out.free(_dev([3]))
+    assert out.device_status() == pkv.PKV_ERR_DEVICE_BOUNDS
+
+
 def test_compact_of_full_and_empty_pools(pkv):
     for rows, add in (([], []), ([0, 1, 2, 3, 4], [24, 24, 24, 24, 24])):
         pool, model = _pair(pkv, 8, 6, 30, 4)

@@ -190,16 +190,16 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p)
     Quad cs{}, sn{};
     if (live && turned) {
         const float *c = p.cos_sin + (int64_t)pos * p.rotary_dim + 4 * l;
-        const float4 x = __ldg(reinterpret_cast<const float4 *>(c));
-        const float4 y = __ldg(reinterpret_cast<const float4 *>(c + p.rotary_dim / 2));
+        const float4 x = *reinterpret_cast<const float4 *>(c);
+        const float4 y = *reinterpret_cast<const float4 *>(c + p.rotary_dim / 2);
         cs = {make_float2(x.x, x.y), make_float2(x.z, x.w)};
         sn = {make_float2(y.x, y.y), make_float2(y.z, y.w)};
     }
     const uint16_t *weight = is_q ? p.q_weight : p.k_weight;
     Quad w0{}, w1{};
     if (weight) {
-        w0 = widen(__ldg(reinterpret_cast<const uint2 *>(weight + c0)));
-        w1 = widen(__ldg(reinterpret_cast<const uint2 *>(weight + c1)));
+        w0 = widen(*reinterpret_cast<const uint2 *>(weight + c0));
+        w1 = widen(*reinterpret_cast<const uint2 *>(weight + c1));
         for (float2 *w : {&w0.a, &w0.b, &w1.a, &w1.b})
             *w = make_float2(w->x + p.weight_offset, w->y + p.weight_offset);
     }

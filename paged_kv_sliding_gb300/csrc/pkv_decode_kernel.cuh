@@ -229,7 +229,7 @@ __global__ void __launch_bounds__(DecTraits<D, TT, KV, TPW>::kThreads, DecTraits
                 if (lp >= n_pages_req ||
                     ((first >= u_hi || first + rows_box <= u_lo) && !(SINK && first < u_sink)))
                     return -1;
-                const int pg = __ldg(p.kv_indices + rq.kv_page_begin + lp);
+                const int pg = p.kv_indices[rq.kv_page_begin + lp];
                 if ((unsigned)pg >= (unsigned)p.num_pages) {
                     record_status(p.status, PKV_ERR_DEVICE_BOUNDS);
                     return -1;
@@ -301,7 +301,7 @@ __global__ void __launch_bounds__(DecTraits<D, TT, KV, TPW>::kThreads, DecTraits
                     uint32_t bytes = 0;
                     if (visible(ts + row)) {
                         const int lp = p.page_shift >= 0 ? (j >> p.page_shift) : j / P;
-                        const int page = __ldg(p.kv_indices + rq.kv_page_begin + lp);
+                        const int page = p.kv_indices[rq.kv_page_begin + lp];
                         if ((unsigned)page < (unsigned)p.num_pages) {
                             off = (((size_t)page * P + (j - lp * P)) * p.num_kv_heads + it.kv_head) *
                                   Tr::kRowBytes;
@@ -344,10 +344,10 @@ __global__ void __launch_bounds__(DecTraits<D, TT, KV, TPW>::kThreads, DecTraits
 #pragma unroll
                 for (int ks = 0; ks < D / 16; ++ks) {
                     const int c = ks * 8 + (lane & 3);  // 32-bit word: columns 2c, 2c+1
-                    qf[ks][0] = v0 ? __ldg(q0 + c) : 0u;
-                    qf[ks][1] = v1 ? __ldg(q1 + c) : 0u;
-                    qf[ks][2] = v0 ? __ldg(q0 + c + 4) : 0u;
-                    qf[ks][3] = v1 ? __ldg(q1 + c + 4) : 0u;
+                    qf[ks][0] = v0 ? *(q0 + c) : 0u;
+                    qf[ks][1] = v1 ? *(q1 + c) : 0u;
+                    qf[ks][2] = v0 ? *(q0 + c + 4) : 0u;
+                    qf[ks][3] = v1 ? *(q1 + c + 4) : 0u;
                 }
             } else {
                 // 8-bit K: the k-slots of k-step ks take the columns 16ks + 4c .. 16ks + 4c + 3
@@ -357,10 +357,10 @@ __global__ void __launch_bounds__(DecTraits<D, TT, KV, TPW>::kThreads, DecTraits
 #pragma unroll
                 for (int ks = 0; ks < D / 16; ++ks) {
                     const int c = ks * 8 + 2 * (lane & 3);
-                    qf[ks][0] = v0 ? __ldg(q0 + c) : 0u;
-                    qf[ks][1] = v1 ? __ldg(q1 + c) : 0u;
-                    qf[ks][2] = v0 ? __ldg(q0 + c + 1) : 0u;
-                    qf[ks][3] = v1 ? __ldg(q1 + c + 1) : 0u;
+                    qf[ks][0] = v0 ? *(q0 + c) : 0u;
+                    qf[ks][1] = v1 ? *(q1 + c) : 0u;
+                    qf[ks][2] = v0 ? *(q0 + c + 1) : 0u;
+                    qf[ks][3] = v1 ? *(q1 + c + 1) : 0u;
                 }
             }
         }

@@ -652,7 +652,7 @@ __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const CopyParams p)
             const int pair = pair0 + step;
             to[u] = -1;
             if (pair < n) {
-                const int a = __ldg(p.src + pair), z = __ldg(p.dst + pair);
+                const int a = p.src[pair], z = p.dst[pair];
                 if (a >= p.num_pages || z >= p.num_pages) {
                     if (p.status)
                         record_status(p.status, PKV_ERR_DEVICE_BOUNDS);

@@ -402,7 +402,7 @@ __global__ void __launch_bounds__(384, 1)
             uint4 hv[D / 16];
 #pragma unroll
             for (int k = 0; k < D / 16; ++k)
-                hv[k] = src ? __ldg(src + k) : make_uint4(0u, 0u, 0u, 0u);
+                hv[k] = src ? src[k] : make_uint4(0u, 0u, 0u, 0u);
             while (qi < item_hi) {
                 if (n_st > 0) {
                     okq = __all_sync(0xffffffffu, mbar_wait(bar(B::kQFree), (n_st - 1) & 1, abort_v, p.wait_ns));
@@ -428,7 +428,7 @@ __global__ void __launch_bounds__(384, 1)
                     if (hf == 0) {
 #pragma unroll
                         for (int k = 0; k < D / 16; ++k)
-                            hv[k] = src ? __ldg(src + D / 16 + k) : make_uint4(0u, 0u, 0u, 0u);
+                            hv[k] = src ? src[D / 16 + k] : make_uint4(0u, 0u, 0u, 0u);
                     }
                 }
                 tmem_wait_st();
@@ -439,7 +439,7 @@ __global__ void __launch_bounds__(384, 1)
                 src = qi < item_hi ? row_src(qi) : nullptr;
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k)
-                    hv[k] = src ? __ldg(src + k) : make_uint4(0u, 0u, 0u, 0u);
+                    hv[k] = src ? src[k] : make_uint4(0u, 0u, 0u, 0u);
             }
             if (!okq) {
                 record_status(p.status, PKV_ERR_TIMEOUT);
@@ -481,7 +481,7 @@ __global__ void __launch_bounds__(384, 1)
                 if (valid) {
     #pragma unroll 4
                     for (int k = 0; k < D / 8; ++k) {
-                        const uint4 v = __ldg(src + k);
+                        const uint4 v = src[k];
                         const uint32_t w4[4] = {v.x, v.y, v.z, v.w};
     #pragma unroll
                         for (int e = 0; e < 4; ++e)
@@ -495,7 +495,7 @@ __global__ void __launch_bounds__(384, 1)
                 const uint32_t qtile = sQ + wg * Tr::kQTileBytes;
     #pragma unroll 4
                 for (int k = 0; k < D / 8; ++k) {
-                    const uint4 v = valid ? __ldg(src + k) : make_uint4(0u, 0u, 0u, 0u);
+                    const uint4 v = valid ? src[k] : make_uint4(0u, 0u, 0u, 0u);
                     const uint32_t w4[4] = {v.x, v.y, v.z, v.w};
                     uint32_t f[4];
     #pragma unroll
@@ -1087,7 +1087,7 @@ __global__ void __launch_bounds__(384, 1)
                                             : j0 / P;
                     if (lp >= n_pages_req)
                         return -1;
-                    const int pg = __ldg(p.kv_indices + rq.kv_page_begin + lp);
+                    const int pg = p.kv_indices[rq.kv_page_begin + lp];
                     if ((unsigned)pg >= (unsigned)p.num_pages) {
                         if (pw == 0)
                             record_status(p.status, PKV_ERR_DEVICE_BOUNDS);
@@ -1207,7 +1207,7 @@ __global__ void __launch_bounds__(384, 1)
                 sl[k] = 0;
                 if (u < 2 * T && jj < rq.kv_len) {
                     const int lp = p.page_shift >= 0 ? (jj >> p.page_shift) : jj / p.page_size;
-                    pg[k] = __ldg(p.kv_indices + rq.kv_page_begin + lp);
+                    pg[k] = p.kv_indices[rq.kv_page_begin + lp];
                     sl[k] = jj - lp * p.page_size;
                 }
             }

@@ -130,6 +130,9 @@ __device__ __forceinline__ float soft_cap_tanh(float y)
 // Programmatic dependent launch: wait until the grids this one depends on have
 // completed and their writes are visible (a no-op for an ordinary launch), and let
 // the next grid in the stream start its own set-up.
+// What such a grid may have written is read with ordinary loads behind the wait: the
+// read-only path (__ldg) wants data that does not change from the kernel's start on, and
+// its loads may move up across the wait.
 __device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
 __device__ __forceinline__ void grid_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory"); }
 

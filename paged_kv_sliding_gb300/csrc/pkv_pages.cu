@@ -375,18 +375,20 @@ __global__ void __launch_bounds__(kApplyThreads) extend_kernel(const PoolParams 
     const int32_t *fresh = p.free_ids + p.first[i];
     if (slots) {
         int64_t *out = slots + p.first_slot[i];
-        // The page that is filled up first. If the entry is none, its tokens have no slot.
-        int last = 0;
+        int last = 0;      // the page that is filled up first
+        int64_t skip = 0;  // its tokens, if the entry is no page id: they have no slot
         if (more > 0 && (unsigned)len % (unsigned)P != 0) {
             last = entries[have - 1];
             if ((unsigned)last >= (unsigned)p.num_pages) {
-                last = -1;
+                skip = min((int64_t)more, (int64_t)have * P - len);
+                for (int64_t t = threadIdx.x; t < skip; t += kApplyThreads)
+                    out[t] = -1;
                 if (threadIdx.x == 0)
                     record_status(p.status, PKV_ERR_DEVICE_BOUNDS);
             }
         }
         constexpr int U = 4;  // tokens of a thread in flight
-        for (int64_t t0 = threadIdx.x; t0 < more; t0 += U * kApplyThreads) {
+        for (int64_t t0 = skip + threadIdx.x; t0 < more; t0 += U * kApplyThreads) {
             int page[U], in[U];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
@@ -399,7 +401,7 @@ __global__ void __launch_bounds__(kApplyThreads) extend_kernel(const PoolParams 
 #pragma unroll
             for (int u = 0; u < U; ++u)
                 if (t0 + u * kApplyThreads < more)
-                    out[t0 + u * kApplyThreads] = page[u] < 0 ? -1 : (int64_t)page[u] * P + in[u];
+                    out[t0 + u * kApplyThreads] = (int64_t)page[u] * P + in[u];
         }
     }
     for (int64_t k = (int64_t)have + threadIdx.x; k < upto; k += kApplyThreads) {

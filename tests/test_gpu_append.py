@@ -215,6 +215,37 @@ def test_v_of_a_bf16_cache_is_v_bit_for_bit(pkv):
         assert (same | torch.isnan(v)).all()
 
 
+SCALES = [0.75, 0.013, 0.021, 0.3, 7 / 1024, 45 / 1024, 3.0, 7.0, 9.37e-5, 1 - 2.0 ** -24, 1 + 2.0 ** -23, 1.1 * 2.0 ** -64,
+          1.5 * 2.0 ** 63, 1.5 * 2.0 ** 64, 1.5 * 2.0 ** -65, 1.5 * 2.0 ** 126, 2.0 ** 127, 2.0 ** -126, 2.0 ** -127,
+          2.0 ** -128, 2.0 ** -149, 3 * 2.0 ** -149]
+
+
+@pytest.mark.parametrize("kv_type", ["bf16", "e4m3", "e5m2"])
+@pytest.mark.parametrize("scale", SCALES)
+def test_values_over_a_scale_are_the_quotients_bit_for_bit(pkv, scale, kv_type):
+    """Every bf16 there is over scales whose reciprocals are rounded (some of the quotients lie
+    halfway between two stored values), at the ends of fp32 and below its normals: the fp32
+    quotient, which numpy gives, rounded once more. k too: neither normalised nor rotated."""
+    v = torch.arange(1 << 16).to(torch.int16).view(torch.bfloat16).view(-1, 2, 64)
+    n = v.shape[0]
+    with np.errstate(all="ignore"):
+        want = torch.from_numpy(v.float().numpy() / np.float32(scale))
+    if kv_type != "bf16":
+        want = want.clamp(-LARGEST[kv_type], LARGEST[kv_type])
+    want = want.to(_dtype(kv_type))
+    raw = torch.int16 if kv_type == "bf16" else torch.uint8
+    caches = [torch.zeros(n // 8, 8, 2, 64, device="cuda").to(_dtype(kv_type)) for _ in range(2)]
+    slots = torch.randperm(n, device="cuda")
+    pkv.norm_rope_append(None, v.cuda(), v.cuda(), slots=slots, k_cache=caches[0], v_cache=caches[1], k_scale=scale,
+                         v_scale=scale)
+    nan = torch.isnan(want.float())
+    for cache in caches:
+        got = cache.view(raw).view(-1, 2, 64)[slots].cpu()
+        assert torch.equal(torch.isnan(got.view(_dtype(kv_type)).float()), nan)
+        off = (got != want.view(raw)) & ~nan
+        assert not off.any(), (int(off.sum()), v[off][:3], got.view(_dtype(kv_type)).float()[off][:3], want.float()[off][:3])
+
+
 def test_bad_slots_and_positions_are_recorded(pkv):
     for name, value in (("slots", 10 ** 9), ("slots", 1 << 40), ("positions", 500), ("positions", -1)):
         s = _inputs(20, 4, 2, 128, 16, 128, "bf16", seed=6)

@@ -228,11 +228,30 @@ def _stream_handle(stream=None) -> int:
     return int(stream.cuda_stream)
 
 
+# Memory of calls on a stream other than the current one. PyTorch gives a dropped tensor's
+# memory to the next one made on the same stream at once, though another stream may still
+# be using it: what the binding makes and keeps for a caller therefore says where it is used.
+
 def _on(stream, *tensors):
-    """The tensors, which were allocated on the current stream, are used on `stream`."""
-    if stream is not None:
-        for t in tensors:
-            t.record_stream(stream)
+    """The tensors are used on `stream`: dropped, they are kept until it has come this far."""
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream.cuda_stream))
+    for t in tensors:
+        t.record_stream(stream)
+
+
+def _made(stream, make, *args, **kw):
+    """A call's result, made by make(...). On an explicit stream it is that stream's own memory
+    (what the current stream has just given up may still be in use there), and the current
+    stream, on which the caller goes on with it, is recorded."""
+    if stream is None:
+        return make(*args, **kw)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream.cuda_stream))
+    with torch.cuda.stream(stream):
+        t = make(*args, **kw)
+    _on(torch.cuda.current_stream(), t)
+    return t
 
 
 def _ptrs(*tensors):
@@ -384,9 +403,9 @@ class Plan:
             if t.dtype != dt or not t.is_cuda or not t.is_contiguous():
                 raise ValueError(f"{name} must be a contiguous CUDA {dt} tensor")
         if out is None:
-            out = torch.empty_like(q)
+            out = _made(stream, torch.empty_like, q)
         if return_lse and lse is None:
-            lse = torch.empty(q.shape[0], q.shape[1], dtype=torch.float32, device=q.device)
+            lse = _made(stream, torch.empty, q.shape[:2], dtype=torch.float32, device=q.device)
         _check(self._lib.pkv_run(self._handle, _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(out),
                                  _ptr(lse), _stream_handle(stream)), "pkv_run")
         return (out, lse) if (return_lse or lse is not None) else out
@@ -429,11 +448,11 @@ def build_kv_indices(req_to_token: torch.Tensor, req_pool_indices: torch.Tensor,
             raise ValueError(f"{name} must be a contiguous CUDA int32 tensor")
     B = kv_lens.numel()
     if kv_indptr is None:
-        kv_indptr = torch.empty(B + 1, dtype=torch.int32, device=kv_lens.device)
+        kv_indptr = _made(stream, torch.empty, (B + 1,), dtype=torch.int32, device=kv_lens.device)
     if kv_indices is None:
         if capacity is None:
             capacity = int(kv_lens.clamp(min=0).sum().item())
-        kv_indices = torch.empty(max(1, capacity), dtype=torch.int32, device=kv_lens.device)
+        kv_indices = _made(stream, torch.empty, (max(1, capacity),), dtype=torch.int32, device=kv_lens.device)
     cap = kv_indices.numel() if capacity is None else min(int(capacity), kv_indices.numel())
     _check(lib.pkv_build_kv_indices(_ptr(req_to_token), req_to_token.shape[0], req_to_token.shape[1],
                                     _ptr(req_pool_indices), _ptr(kv_start), _ptr(kv_lens), B, _ptr(loc_map),
@@ -542,8 +561,7 @@ def norm_rope_append(q: Optional[torch.Tensor], k: Optional[torch.Tensor], v: Op
     eps, weight_offset, k_scale, v_scale = float(eps), float(weight_offset), float(k_scale), float(v_scale)
     interleaved = bool(interleaved)
     if q is not None and q_out is None:
-        q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
-        _on(stream, q_out)
+        q_out = _made(stream, torch.empty, q.shape, dtype=torch.bfloat16, device=q.device)
     dev = torch.cuda.current_device()
     tensors = (q, k, v, q_weight, k_weight, cos_sin, positions, slots, q_out, k_out, k_cache, v_cache, status)
     key = (dev, eps, weight_offset, interleaved, k_scale, v_scale) + tuple(map(_sig, tensors))
@@ -560,9 +578,10 @@ def norm_rope_append(q: Optional[torch.Tensor], k: Optional[torch.Tensor], v: Op
 class PagePool:
     """The pages of a cache on the device: table [rows, max_pages] page ids, lens [rows]
     tokens and refs [num_pages] int32 (how many table entries in use name a page; 0: free),
-    all CUDA tensors that stay the caller's. Calls are asynchronous on the current stream;
-    what they could not do is in device_status(). A pool's calls share its workspace, so
-    they must not overlap on several streams."""
+    all CUDA tensors that stay the caller's. Calls are asynchronous on the current stream, or
+    on `stream`, which the caller orders behind the one that the pool was made on; what they
+    could not do is in device_status(). A pool's calls share its workspace, so they must not
+    overlap on several streams; a pool outlives the graphs that its calls were captured in."""
 
     def __init__(self, table: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor, *, page_size: int):
         self._lib = load_library()
@@ -582,12 +601,21 @@ class PagePool:
         d.row_stride, d.num_rows, d.num_pages, d.page_size = table.shape[1], table.shape[0], refs.shape[0], self.page_size
         d.workspace, d.workspace_bytes, d.status = self._workspace.data_ptr(), size.value, self._status.data_ptr()
         self._desc = d
+        self._home = _stream_handle()  # the stream whose memory this is
 
     @classmethod
     def empty(cls, *, num_rows: int, max_pages: int, num_pages: int, page_size: int, device="cuda") -> "PagePool":
         """A pool without tokens."""
         zeros = lambda *shape: torch.zeros(shape, dtype=torch.int32, device=device)  # noqa: E731
         return cls(zeros(num_rows, max_pages), zeros(num_rows), zeros(num_pages), page_size=page_size)
+
+    def _used_on(self, stream) -> int:
+        """The handle of a call's stream, which from now on may be using the pool's memory."""
+        handle = _stream_handle(stream)
+        if handle != self._home:
+            _on(torch.cuda.current_stream() if stream is None else stream, self.table, self.lens, self.refs,
+                self._workspace, self._status)
+        return handle
 
     def _index(self, *tensors):
         if torch.cuda.current_device() != self._device:
@@ -604,13 +632,12 @@ class PagePool:
         slots are returned, entry after entry."""
         n = self._index(rows, add)
         if slots is None and total is not None:
-            slots = torch.empty(total, dtype=torch.int64, device=self.table.device)
-            _on(stream, slots)
+            slots = _made(stream, torch.empty, (total,), dtype=torch.int64, device=self.table.device)
         elif slots is not None:
             _want(slots, "slots", torch.int64)
         _check(self._lib.pkv_pages_extend(self._desc, rows.data_ptr(), add.data_ptr(), n,
                                           None if slots is None else slots.data_ptr(),
-                                          0 if slots is None else slots.numel(), _stream_handle(stream)),
+                                          0 if slots is None else slots.numel(), self._used_on(stream)),
                "pkv_pages_extend")
         return slots
 
@@ -618,18 +645,17 @@ class PagePool:
              dst: Optional[torch.Tensor] = None, stream=None):
         """children[i], an empty row, becomes a copy of parents[i]: full pages are shared, a
         partly filled last one is new. Returns (src, dst), the pages to copy (or -1)."""
-        src = torch.empty_like(parents) if src is None else src
-        dst = torch.empty_like(parents) if dst is None else dst
-        _on(stream, src, dst)
+        src = _made(stream, torch.empty, parents.shape, dtype=torch.int32, device=parents.device) if src is None else src
+        dst = _made(stream, torch.empty, parents.shape, dtype=torch.int32, device=parents.device) if dst is None else dst
         n = self._index(parents, children, src, dst)
         _check(self._lib.pkv_pages_fork(self._desc, parents.data_ptr(), children.data_ptr(), n, src.data_ptr(),
-                                        dst.data_ptr(), _stream_handle(stream)), "pkv_pages_fork")
+                                        dst.data_ptr(), self._used_on(stream)), "pkv_pages_fork")
         return src, dst
 
     def free(self, rows: torch.Tensor, stream=None):
         """The rows become empty; pages that no other row names are free again."""
         n = self._index(rows)
-        _check(self._lib.pkv_pages_free(self._desc, rows.data_ptr(), n, _stream_handle(stream)), "pkv_pages_free")
+        _check(self._lib.pkv_pages_free(self._desc, rows.data_ptr(), n, self._used_on(stream)), "pkv_pages_free")
 
     def compact(self, out: Optional["PagePool"] = None, src: Optional[torch.Tensor] = None,
                 dst: Optional[torch.Tensor] = None, count: Optional[torch.Tensor] = None, stream=None):
@@ -638,16 +664,17 @@ class PagePool:
         device. The caches' pages are the caller's to copy (copy_pages) before the new
         table is used."""
         if src is None:
-            src = torch.empty(self.refs.shape[0] // 2, dtype=torch.int32, device=self.table.device)
+            src = _made(stream, torch.empty, (self.refs.shape[0] // 2,), dtype=torch.int32, device=self.table.device)
         if dst is None:
-            dst = torch.empty_like(src)
+            dst = _made(stream, torch.empty, src.shape, dtype=torch.int32, device=self.table.device)
         if count is None:
-            count = torch.empty(1, dtype=torch.int32, device=self.table.device)
-        _on(stream, src, dst, count)
+            count = _made(stream, torch.empty, (1,), dtype=torch.int32, device=self.table.device)
         n = self._index(src, dst)
         self._index(count)
-        _check(self._lib.pkv_pages_compact(self._desc, (out or self)._desc, src.data_ptr(), dst.data_ptr(), n,
-                                           count.data_ptr(), _stream_handle(stream)), "pkv_pages_compact")
+        out = self if out is None else out
+        out._used_on(stream)
+        _check(self._lib.pkv_pages_compact(self._desc, out._desc, src.data_ptr(), dst.data_ptr(), n,
+                                           count.data_ptr(), self._used_on(stream)), "pkv_pages_compact")
         return src, dst, count
 
     def device_status(self) -> int:
@@ -704,9 +731,9 @@ def merge_state(v_a: torch.Tensor, s_a: torch.Tensor, v_b: torch.Tensor, s_b: to
     if v_a.shape != v_b.shape or v_a.dim() != 3 or s_a.shape != v_a.shape[:2] or s_b.shape != s_a.shape:
         raise ValueError("shape mismatch")
     if v_out is None:
-        v_out = torch.empty_like(v_a)
+        v_out = _made(stream, torch.empty_like, v_a)
     if s_out is None:
-        s_out = torch.empty_like(s_a)
+        s_out = _made(stream, torch.empty_like, s_a)
     dtype = PKV_BF16 if v_a.dtype == torch.bfloat16 else PKV_F32
     _check(lib.pkv_merge_state(_ptr(v_a), _ptr(s_a), _ptr(v_b), _ptr(s_b), _ptr(v_out), _ptr(s_out),
                                v_a.shape[0], v_a.shape[1], v_a.shape[2], dtype,

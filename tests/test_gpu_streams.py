@@ -1,0 +1,123 @@
+"""Calls on a stream other than the current one, while that stream or the current one is busy:
+what the binding makes for a call is not memory that is still in use, and is not handed
+out again before the call is done with it."""
+from __future__ import annotations
+
+import pytest
+import torch
+
+from paged_kv_sliding_gb300 import inputs
+
+pytestmark = pytest.mark.gpu
+
+BUSY = 60_000_000  # clock ticks: about 30 ms
+
+
+@pytest.fixture(scope="module")
+def pkv():
+    from paged_kv_sliding_gb300 import build, pkv as binding
+    build.build()
+    binding.load_library()
+    return binding
+
+
+def _i32(*x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def _fill_all(size, n=64):
+    """Tensors of `size` bytes from the current stream's memory, what was just dropped first."""
+    return [torch.full((size,), 77, dtype=torch.uint8, device="cuda") for _ in range(n)]
+
+
+@pytest.mark.parametrize("how", ["explicit", "current"])
+def test_a_pool_dropped_behind_its_call(pkv, how):
+    side = torch.cuda.Stream()
+    rows, add = _i32(0, 1, 2), _i32(40, 9, 100)
+    for call in (lambda p, s: p.extend(rows, add, total=149, stream=s), lambda p, s: p.free(rows, stream=s),
+                 lambda p, s: p.compact(stream=s), lambda p, s: p.fork(rows[:1], rows[2:], stream=s)):
+        pool = pkv.PagePool.empty(num_rows=4, max_pages=400, num_pages=900, page_size=4)
+        sizes = {t.numel() * t.element_size() for t in (pool.table, pool.lens, pool.refs, pool._workspace, pool._status)}
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(BUSY)
+            got = call(pool, None) if how == "current" else None
+        if how == "explicit":
+            got = call(pool, side)
+        del pool, got
+        marks = [m for size in sizes for m in _fill_all(size)]
+        side.synchronize()
+        assert all((m == 77).all() for m in marks)
+
+
+def _calls(pkv):
+    """Calls that make their results, over inputs that lie ready."""
+    w = inputs.tiny_extend().to("cuda")
+    plan = pkv.plan_for(w)
+    k = torch.randn(64, 4, 64, device="cuda").to(torch.bfloat16)
+    s = torch.randn(64, 4, device="cuda")
+    pool = pkv.PagePool.empty(num_rows=4, max_pages=40, num_pages=90, page_size=4)
+    table = torch.arange(400, dtype=torch.int32, device="cuda").view(4, 100)
+    calls = {"run": lambda st: plan.run(w.q, w.k_cache, w.v_cache, return_lse=True, stream=st),
+             "append": lambda st: (pkv.norm_rope_append(k, None, q_weight=k[0, 0].contiguous(), stream=st),),
+             "merge": lambda st: pkv.merge_state(k, s, k, s, stream=st),
+             "indices": lambda st: pkv.build_kv_indices(table, _0123, _0123, _60s, capacity=240, stream=st),
+             "extend": lambda st: (pool.extend(_0123[:2], _60s[:2], total=120, stream=st),)}
+    _0123, _60s = _i32(0, 1, 2, 3), _i32(60, 60, 60, 60)
+    return calls, pool
+
+
+@pytest.mark.parametrize("name", ["run", "append", "merge", "indices", "extend"])
+def test_results_are_not_memory_that_the_current_stream_still_reads(pkv, name):
+    calls, _ = _calls(pkv)
+    side = torch.cuda.Stream()
+    for t in calls[name](None):  # a tensor of each result's size
+        size = t.numel() * t.element_size()
+        marks = _fill_all(size)
+        copies = [torch.empty_like(m) for m in marks]
+        torch.cuda.synchronize()
+        torch.cuda._sleep(BUSY)
+        for m, c in zip(marks, copies):
+            c.copy_(m)
+        del marks, m
+        got = calls[name](side)  # its inputs lie ready: nothing to wait for
+        side.synchronize()
+        torch.cuda.synchronize()
+        assert all((c == 77).all() for c in copies)
+        del got
+
+
+@pytest.mark.parametrize("name", ["run", "append", "merge", "indices", "extend"])
+def test_results_dropped_behind_their_call(pkv, name):
+    calls, _ = _calls(pkv)
+    side = torch.cuda.Stream()
+    sizes = {t.numel() * t.element_size() for t in calls[name](None)}
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(BUSY)
+    calls[name](side)
+    with torch.cuda.stream(side):  # the next tensors of that stream follow the call
+        later = [m for size in sizes for m in _fill_all(size)]
+    marks = [m for size in sizes for m in _fill_all(size)]
+    torch.cuda.synchronize()
+    assert all((m == 77).all() for m in marks + later)
+
+
+def test_results_dropped_while_the_current_stream_reads_them(pkv):
+    """Made on the side stream, read on the current one, dropped: not written again by the
+    side stream's next call until they are read."""
+    calls, _ = _calls(pkv)
+    side = torch.cuda.Stream()
+    want = [t.clone() for t in calls["run"](None)]
+    torch.cuda.synchronize()
+    got = calls["run"](side)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda._sleep(BUSY)
+    copies = [t.clone() for t in got]
+    sizes = [t.numel() * t.element_size() for t in got]
+    del got
+    with torch.cuda.stream(side):
+        later = [m for size in sizes for m in _fill_all(size)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(want, copies)) and all((m == 77).all() for m in later)

@@ -910,8 +910,11 @@ int pkv_plan_device_status(const pkv_plan *plan, int32_t *status)
     cudaError_t ce = cudaDeviceSynchronize();
     if (ce == cudaSuccess)
         ce = cudaMemcpy(&h, plan->d_status, sizeof h, cudaMemcpyDeviceToHost);
+    // cleared before the next run, on whatever stream, can record anything
     if (ce == cudaSuccess)
         ce = cudaMemset(plan->d_status, 0, sizeof(int32_t));
+    if (ce == cudaSuccess)
+        ce = cudaDeviceSynchronize();
     if (ce != cudaSuccess)
         return cuda_fail(ce, "reading the device status");
     *status = h;

@@ -682,6 +682,8 @@ class PagePool:
         torch.cuda.synchronize(self.table.device)
         st = int(self._status.item())
         self._status.zero_()
+        # cleared before the next call, on whatever stream, can record anything
+        torch.cuda.synchronize(self.table.device)
         return st
 
 

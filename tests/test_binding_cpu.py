@@ -189,3 +189,15 @@ def test_results_of_a_call_on_a_stream_are_its_own_memory(streams, name):
     got = RESULTS[name](pool, None)
     for t in got if isinstance(got, tuple) else (got,):
         assert t.home is main and t.used == {main}
+
+
+def test_a_pools_status_is_clear_when_it_has_been_read(streams, monkeypatch):
+    """The clearing write is waited for: on its own stream it could erase what a call queued
+    next on another stream records."""
+    pool = _pool()
+    order = []
+    monkeypatch.setattr(torch.cuda, "synchronize", lambda device=None: order.append("wait"))
+    monkeypatch.setattr(OnDevice, "item", lambda self: order.append("read") or 5, raising=False)
+    monkeypatch.setattr(OnDevice, "zero_", lambda self: order.append("clear") or self, raising=False)
+    assert pool.device_status() == 5
+    assert order == ["wait", "read", "clear", "wait"]

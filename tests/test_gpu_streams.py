@@ -121,3 +121,27 @@ def test_results_dropped_while_the_current_stream_reads_them(pkv):
         later = [m for size in sizes for m in _fill_all(size)]
     torch.cuda.synchronize()
     assert all(torch.equal(x, y) for x, y in zip(want, copies)) and all((m == 77).all() for m in later)
+
+
+def test_a_status_that_was_read_does_not_erase_the_next(pkv):
+    """Read and clear, then at once a call on another stream that has something to record."""
+    w = inputs.batch_decode(127, batch=8).to("cuda")
+    plan = pkv.plan_for(w)
+    good, side = plan._kv_indices.clone(), torch.cuda.Stream()
+    plan._kv_indices.fill_(10 ** 6)  # no page: recorded, not read
+    pool = pkv.PagePool.empty(num_rows=2, max_pages=2, num_pages=2, page_size=4)
+    out, lse = torch.empty_like(w.q), torch.empty(w.q.shape[:2], device="cuda")
+    nobody = _i32(7)
+    torch.cuda.synchronize()
+    for _ in range(200):
+        assert plan.device_status() in (pkv.PKV_OK, pkv.PKV_ERR_DEVICE_BOUNDS)
+        plan.run(w.q, w.k_cache, w.v_cache, out, lse, stream=side)
+        assert plan.device_status() == pkv.PKV_ERR_DEVICE_BOUNDS
+        assert pool.device_status() == pkv.PKV_OK
+        pool.free(nobody, stream=side)
+        assert pool.device_status() == pkv.PKV_ERR_DEVICE_BOUNDS
+    plan._kv_indices.copy_(good)
+    torch.cuda.synchronize()
+    assert plan.device_status() == pkv.PKV_OK
+    plan.run(w.q, w.k_cache, w.v_cache, out, lse)
+    assert plan.device_status() == pkv.PKV_OK

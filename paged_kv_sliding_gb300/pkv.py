@@ -635,6 +635,7 @@ class PagePool:
             slots = _made(stream, torch.empty, (total,), dtype=torch.int64, device=self.table.device)
         elif slots is not None:
             _want(slots, "slots", torch.int64)
+            _here(self._device, slots)
         _check(self._lib.pkv_pages_extend(self._desc, rows.data_ptr(), add.data_ptr(), n,
                                           None if slots is None else slots.data_ptr(),
                                           0 if slots is None else slots.numel(), self._used_on(stream)),
@@ -672,6 +673,8 @@ class PagePool:
         n = self._index(src, dst)
         self._index(count)
         out = self if out is None else out
+        if out._device != self._device:
+            raise ValueError(f"the pools are on cuda:{self._device} and cuda:{out._device}")
         out._used_on(stream)
         _check(self._lib.pkv_pages_compact(self._desc, out._desc, src.data_ptr(), dst.data_ptr(), n,
                                            count.data_ptr(), self._used_on(stream)), "pkv_pages_compact")

@@ -201,3 +201,27 @@ def test_a_pools_status_is_clear_when_it_has_been_read(streams, monkeypatch):
     monkeypatch.setattr(OnDevice, "zero_", lambda self: order.append("clear") or self, raising=False)
     assert pool.device_status() == 5
     assert order == ["wait", "read", "clear", "wait"]
+
+
+class OnAnother(OnDevice):
+    """A host tensor that says it is on cuda:1, which is not the current device."""
+
+    device = property(lambda self: torch.device("cuda", 1))
+
+    def get_device(self):
+        return 1
+
+
+def test_a_pools_calls_refuse_memory_of_another_device(streams, lib, monkeypatch):
+    pool = _pool()
+    with monkeypatch.context() as there:
+        there.setattr(torch.cuda, "current_device", lambda: 1)
+        zeros = [torch.zeros(*n, dtype=torch.int32).as_subclass(OnAnother) for n in ((4, 3), (4,), (8,))]
+        other = pkv.PagePool(*zeros, page_size=4)
+    lib.calls.clear()
+    slots = torch.zeros(2, dtype=torch.int64).as_subclass(OnAnother)
+    for bad in (lambda: pool.extend(_ints(2), _ints(2), slots=slots), lambda: pool.compact(out=other),
+                lambda: pool.free(_ints(2).as_subclass(OnAnother)), lambda: other.free(_ints(2))):
+        with pytest.raises(ValueError, match="cuda:1|device"):
+            bad()
+    assert not lib.calls

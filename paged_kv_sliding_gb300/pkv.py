@@ -240,15 +240,20 @@ def _on(stream, *tensors):
         t.record_stream(stream)
 
 
+def _within(stream):
+    """The torch operations of a block go to `stream` (None: the current one)."""
+    if stream is not None and not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream.cuda_stream))
+    return torch.cuda.stream(stream)
+
+
 def _made(stream, make, *args, **kw):
     """A call's result, made by make(...). On an explicit stream it is that stream's own memory
     (what the current stream has just given up may still be in use there), and the current
     stream, on which the caller goes on with it, is recorded."""
     if stream is None:
         return make(*args, **kw)
-    if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream.cuda_stream))
-    with torch.cuda.stream(stream):
+    with _within(stream):
         t = make(*args, **kw)
     _on(torch.cuda.current_stream(), t)
     return t
@@ -451,7 +456,8 @@ def build_kv_indices(req_to_token: torch.Tensor, req_pool_indices: torch.Tensor,
         kv_indptr = _made(stream, torch.empty, (B + 1,), dtype=torch.int32, device=kv_lens.device)
     if kv_indices is None:
         if capacity is None:
-            capacity = int(kv_lens.clamp(min=0).sum().item())
+            with _within(stream):  # behind whatever writes them there
+                capacity = int(kv_lens.clamp(min=0).sum().item())
         kv_indices = _made(stream, torch.empty, (max(1, capacity),), dtype=torch.int32, device=kv_lens.device)
     cap = kv_indices.numel() if capacity is None else min(int(capacity), kv_indices.numel())
     _check(lib.pkv_build_kv_indices(_ptr(req_to_token), req_to_token.shape[0], req_to_token.shape[1],

@@ -145,3 +145,18 @@ def test_a_status_that_was_read_does_not_erase_the_next(pkv):
     assert plan.device_status() == pkv.PKV_OK
     plan.run(w.q, w.k_cache, w.v_cache, out, lse)
     assert plan.device_status() == pkv.PKV_OK
+
+
+def test_lengths_of_the_page_list_are_read_behind_what_writes_them(pkv):
+    """No capacity given: it is read from kv_lens, which the call's stream is about to write."""
+    table = torch.arange(40, dtype=torch.int32, device="cuda").view(4, 10)
+    rows, start, lens, more = _i32(3, 0), _i32(0, 2), _i32(0, 0), _i32(4, 5)
+    side = torch.cuda.Stream()
+    pkv.build_kv_indices(table, rows, start, lens)  # (kernels loaded on their first use wait for the device)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(BUSY)
+        lens.copy_(more)
+    indptr, indices = pkv.build_kv_indices(table, rows, start, lens, stream=side)
+    side.synchronize()
+    assert indptr.tolist() == [0, 4, 9] and indices.tolist() == [30, 31, 32, 33, 2, 3, 4, 5, 6]

@@ -114,6 +114,68 @@ def test_a_large_pool(pkv):
     _same(pool, model, "compact")
 
 
+@pytest.mark.parametrize("n", [8192, 8193, 10001, 20000])
+def test_calls_of_many_entries(pkv, n):
+    """More than 32 entries to a warp of the ranking (8192 in all), repeated and refused ones in
+    either of a warp's groups and across warps."""
+    rng = np.random.default_rng(n)
+    rows, cols, P = n + 50, 4, 3
+    pool, model = _pair(pkv, rows, cols, 3 * n, P)
+    who, add = rng.permutation(rows)[:n], rng.integers(0, 2 * P + 1, size=n)
+    per = -(-n // 256)  # entries of a warp
+
+    def extend(who, add, what):
+        nonlocal model
+        slots = torch.empty(int(np.sum(add)) + 3, dtype=torch.int64, device="cuda")
+        model, out = _both(lambda: pool.extend(_dev(who), _dev(add), slots=slots), lambda: model.extend(who, add), pool,
+                           model, what)
+        assert slots.cpu().tolist() == (out[0] if out else [-1] * int(np.sum(add))) + [-1] * 3, what
+        return out
+
+    assert extend(who, add, "extend")
+    for i, j in ((per, 2 * per - 1), (per + 1, n - 1), (2 * per - 1, n - 2), (0, 31 % per)):
+        twice = who.copy()
+        twice[j] = twice[i]
+        assert not extend(twice, add, f"entries {i} and {j}")
+    for i in (n - 1, 2 * per - 1):
+        far = add.copy()
+        far[i] = cols * P + 1
+        assert not extend(who, far, f"entry {i} beyond its row")
+    assert extend(who, np.minimum(add, 1), "again")
+    empty, full = np.flatnonzero(model.lens == 0), np.flatnonzero(model.lens)
+    model = model.free(full[:: 2])
+    pool.free(_dev(full[:: 2]))
+    children = np.concatenate([empty, full[:: 2]])
+    children = rng.permutation(np.concatenate([children, np.flatnonzero(model.lens)[: max(0, n - len(children))]]))
+    extra = [int(r) for r in children if model.lens[r]]
+    model = model.free(extra)
+    pool.free(_dev(extra))
+    parents = rng.integers(0, rows, size=len(children))
+    got = []
+    for i, j in ((0, len(children) - 1), (33, 40)):
+        twice = children.copy()
+        twice[j] = twice[i]
+        _both(lambda: pool.fork(_dev(parents), _dev(twice)), lambda: model.fork(parents, twice), pool, model, "fork twice")
+    model, out = _both(lambda: got.append(pool.fork(_dev(parents), _dev(children))) or got[0],
+                       lambda: model.fork(parents, children), pool, model, "fork")
+    assert out and [x.cpu().tolist() for x in got[0]] == out
+
+
+@pytest.mark.parametrize("P", [1, 16, 7, 1000])
+def test_slots_of_rows_that_grow_by_many_tokens(pkv, P):
+    """Around the tokens that a CTA writes in one pass, from lengths inside a page and at its
+    end, and growth within one page."""
+    first = np.array([1, P, P + 1, 3 * P - 1, 5, 999, 0, 2 * P, 11], dtype=np.int64)
+    add = np.array([1023, 1024, 1025, 5000, 4096, 1, 2049, 3073, 0], dtype=np.int64)
+    pool, model = _pair(pkv, len(first), 15000 // P + 4, 40000 // P + 60, P)
+    who = np.random.default_rng(P).permutation(len(first))
+    for some in (first, add, add[::-1].copy()):
+        slots = torch.full((int(some.sum()) + 5,), 77, dtype=torch.int64, device="cuda")
+        model, out = _both(lambda: pool.extend(_dev(who), _dev(some), slots=slots), lambda: model.extend(who, some), pool,
+                           model, "extend")
+        assert out and slots.cpu().tolist() == out[0] + [-1] * 5
+
+
 def _filled(pkv, P=4):
     pool, model = _pair(pkv, 8, 6, 30, P)
     rows, add = [0, 3, 5, 6], [9, 8, 1, 17]

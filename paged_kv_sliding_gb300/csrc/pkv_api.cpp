@@ -518,10 +518,10 @@ void build_schedule(const pkv_plan_desc &d, const std::vector<HostRequest> &reqs
         auto keys = [](const DecodeItem &it) { return it.sink_end + it.j1 - it.j0; };
         std::stable_sort(d_items.begin(), d_items.end(),
                          [&](const DecodeItem &a, const DecodeItem &b) { return keys(a) > keys(b); });
+        const auto tile_for = sinks > 0 ? decode_sinks_tile_for : decode_tile_for;
         decode_tile = fixed_tile > 0 ? fixed_tile
-                                     : decode_tile_for(d.head_dim,
-                                                       d_items.empty() ? 0 : keys(d_items.front()),
-                                                       (int64_t)d_items.size(), device_sm_count(device), sinks > 0);
+                                     : tile_for(d.head_dim, d_items.empty() ? 0 : keys(d_items.front()),
+                                                (int64_t)d_items.size(), device_sm_count(device));
     }
     sc.num_partials = num_partials;
     sc.num_counters = num_counters;

@@ -203,24 +203,37 @@ cudaError_t launch_decode(const DecodeParams &p, int head_dim, int num_items, cu
 // short key ranges, which are latency-bound, and for medium ones (<= 1024 keys)
 // whose CTAs need more than one wave at 2 per SM but fit in one at 4; otherwise 64
 // (twice the bytes in flight per CTA, which long ranges need).
-// Plans with sinks have a rule of their own for the medium ranges, whose bound a window
-// of 1024 keys and its sinks would just miss: up to 1536 keys from 2.25 items per SM on,
-// 640 below. Measured, 32 against 64: 512 items of 1028 keys 41.1 / 45.2 us (E4M3 25.3 /
-// 32.2), 1405 keys 51.3 / 56.2, 352 items of 1028 keys 30.7 / 38.2; 512 items of 2005 keys
-// 62.6 / 61.5; 312 items of 505 keys 15.3 / 16.7, of 1028 keys 27.6 / 26.0 (E4M3 22.4 / 16.2).
-inline int decode_tile_for(int head_dim, int64_t max_keys, int64_t n_items, int n_sm, bool sinks = false)
+inline int decode_tile_for(int head_dim, int64_t max_keys, int64_t n_items, int n_sm)
 {
     if (head_dim > 128)
         return 64;
     if (max_keys <= 192)
         return 32;
-    if (sinks)
-        return n_items > 2LL * n_sm && n_items <= 4LL * n_sm && max_keys <= (4 * n_items > 9LL * n_sm ? 1536 : 640) ? 32
-                                                                                                                : 64;
     if (max_keys <= 1024 && n_items > 2LL * n_sm && n_items <= 4LL * n_sm)
         return 32;
     return 64;
 }
+
+// The same for plans with sinks, whose kernels are others: 64 while the items fit in one wave
+// of such CTAs (2 on an SM at head_dim 128, 3 at 64), 32, of which an SM holds twice as many,
+// beyond, for ranges of up to 1536 keys (640 just above one wave). Measured, 32 against 64 in
+// us, 8 KV heads, pages of 16, bf16 (or E4M3): d 128, 8 items of 132 keys 5.65 / 4.81, 304
+// of 132 6.82 / 6.06, 512 of 132 7.45 / 11.33, 312 of 505 15.3 / 16.7, of 1028 28.3 / 26.8,
+// 512 of 1028 41.1 / 45.9 (26.1 / 32.2), of 2005 63.0 / 61.6; d 64, 352 of 1028 23.7 / 17.1
+// (448: 18.8 / 15.1), 512 of 505 14.4 / 18.3, 608 of 1028 26.9 / 34.8. Over 1684 measured
+// batches (1 to 200 requests, 9 to 2005 keys, pages of 1, 5, 16 and 64) the choice is within
+// 5% of the better one in 1532 and 1.3% slower in the mean; it loses most where lengths
+// happen to fill the other's waves (384 items of 1405 keys, E4M3: 29.5 / 24.1), on E4M3 ranges
+// of some 20 keys (3.7 / 4.5 at d 64) and beyond 1536 keys with gathered pages (d 64, E4M3,
+// pages of 5, 608 items of 1705 keys: 46.9 / 73.6).
+inline int decode_sinks_tile_for(int head_dim, int64_t max_keys, int64_t n_items, int n_sm)
+{
+    const int wave = head_dim == 64 ? 3 : 2;  // items per SM
+    if (head_dim > 128 || n_items <= (int64_t)wave * n_sm)
+        return 64;
+    return max_keys <= (4 * n_items > (4LL * wave + 1) * n_sm ? 1536 : 640) ? 32 : 64;
+}
+
 // KV tokens per stage of the decode kernel that runs a plan's tile variant (32: short
 // key ranges; 64: the rest): 8-bit caches at head_dim <= 128 run both variants with
 // two 16-token sub-blocks per compute warp, so their stages are twice as long (64 and

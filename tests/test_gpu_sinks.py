@@ -87,6 +87,33 @@ def test_decode(pkv, oracle_lib, d, P, kv_type):
         _check(oracle_lib, w, out, lse, sinks, f"d {d} P {P} {kv_type} W {W} sinks {sinks}")
 
 
+@pytest.mark.parametrize("kv_type", ["bf16", "e4m3", "e5m2"])
+@pytest.mark.parametrize("P", [1, 5, 16, 64, 128])
+@pytest.mark.parametrize("d", [64, 128])
+def test_decode_of_more_than_one_wave(pkv, oracle_lib, d, P, kv_type):
+    """More items than SMs hold of the CTAs with long stages: those with short ones."""
+    B = 3 * torch.cuda.get_device_properties(0).multi_processor_count // 8 + 1
+    kv = np.random.default_rng(d + P).integers(1, 400, size=B)
+    for W, sinks in ((0, 1), (31, 4), (100, 70)):
+        w = _workload("decode", d + P, [1] * B, kv, W, d=d, P=P, heads=(16, 8))
+        w = w if kv_type == "bf16" else wl.to_kv8(w, kv_type)
+        out, lse, plan = _run(pkv, w, sinks)
+        assert plan.info["kv_tile"] == (32 if kv_type == "bf16" else 64)
+        _check(oracle_lib, w, out, lse, sinks, f"d {d} P {P} {kv_type} W {W} sinks {sinks}")
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_decode_stages_of_one_wave_and_beyond(pkv, d):
+    """Long stages as long as their CTAs fit in one wave (2 items to an SM, 3 at d 64)."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    one = (3 if d == 64 else 2) * sms
+    for items, keys, tile in ((1, 100, 64), (one, 100, 64), (one, 700, 64), (one + 1, 100, 32), (one + 1, 640, 32),
+                              (one + 1, 641, 64), (one + sms // 4 + 1, 1536, 32), (one + sms // 4 + 1, 1537, 64)):
+        w = _workload("decode", 1, [1] * items, [2000] * items, keys - 5, d=d, P=16, heads=(1, 1))
+        plan = pkv.plan_for(w.to("cuda"), num_sinks=4, disable_split_kv=True)
+        assert plan.info["num_work_items"] == items and plan.info["kv_tile"] == tile, (items, keys)
+
+
 @pytest.mark.parametrize("split", [1, 16, 50, 64, 300])
 @pytest.mark.parametrize("P", [1, 16])
 def test_decode_splits_across_the_gap(pkv, oracle_lib, P, split):

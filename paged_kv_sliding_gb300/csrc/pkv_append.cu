@@ -288,17 +288,22 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p)
     }
 }
 
-// Values of q, k and v below which a lane group takes one head, otherwise kManyHeads.
-// Measured, one head against four: 6144 rows of 128 2.18 / 2.48 us, 12288 2.99 / 2.69; 2048
-// rows of 256 1.97 / 2.47 us, 4096 2.69 / 2.58; 12288 rows of 64 2.13 / 2.58 us, 24576
-// 2.99 / 3.36.
+// Values of q, k and v below which a lane group takes one head, otherwise kManyHeads; a call
+// without two heads in any tensor, whose groups of four would stay three quarters empty,
+// takes one at any size. Measured in us, one head against four, bf16: 32 + 2 x 8 heads of
+// 64, 12288 rows 2.12 / 2.49, 16384 2.83 / 2.49, 24576 2.93 / 2.70; of 128, 4096 rows 1.97 /
+// 2.39, 8192 2.79 / 2.57; of 256, 4096 rows 2.81 / 2.58, 65536 17.8 / 9.6; 1 + 2 x 1 heads of
+// 128, 8192 rows 2.68 / 2.77, 196608 26.4 / 30.4. Heads that fill half of their groups lose
+// between 1.4 and 2.1 million values (5 + 2 x 1 of 64, 24576 rows 2.89 / 3.50; 32768 3.29 /
+// 3.54) and gain on either side (2 + 2 x 2, 16384 rows 2.67 / 2.27, 49152 4.11 / 3.52).
 constexpr int kManyHeads = 4;
 constexpr int64_t kFewValues = 1 << 20;
 
 template <int D, int KV, bool INTERLEAVED>
 cudaError_t launch_di(AppendParams p, cudaStream_t s)
 {
-    const bool few = (int64_t)p.num_tokens * (p.num_qo_heads + 2 * p.num_kv_heads) * D < kFewValues;
+    const bool few = (p.num_qo_heads <= 1 && p.num_kv_heads <= 1) ||
+                     (int64_t)p.num_tokens * (p.num_qo_heads + 2 * p.num_kv_heads) * D < kFewValues;
     const int hpg = few ? 1 : kManyHeads;
     const int kv_chunks = (p.num_kv_heads + hpg - 1) / hpg;
     p.chunks = (p.num_qo_heads + hpg - 1) / hpg + (p.k_cache ? 2 : 1) * kv_chunks;

@@ -19,9 +19,10 @@
 //   - a lane group takes HPG heads of one token and one tensor: rows, slot and position are
 //     all in flight at once, and weights, cos and sin are loaded once for HPG rows.
 // HPG = 1 for few rows (latency: a decode step of 64 tokens x 48 heads spreads over all
-// SMs, 2.1 us), HPG = 4 otherwise. Measured on 16384 tokens x 48 heads of 128, bf16: 64.7 us
-// = 6.36 TB/s, 0.94 of the copy rate (eight heads 62 us there, but 23.4
-// against 22.0 us on 8191 tokens of 8 + 2 x 4 heads, where they stay half empty).
+// SMs, 2.1 us), HPG = 4 otherwise. Measured on 16384 tokens x 48 heads of 128, bf16: 64.5 us
+// = 6.37 TB/s, 0.94 of the copy rate; 8191 tokens of 8 + 2 x 4 heads of 256 into E4M3 22.5 us
+// (with products by one rounded reciprocal 22.15; eight heads to a group, measured with
+// those, 62 and 23.4 us: on the second they stay half empty).
 #include <cmath>
 #include <string>
 
@@ -116,7 +117,7 @@ __device__ __forceinline__ float divide(float a, float b)
 // middle of two. (Not below 2^-100, where x lo loses bits; an 8-bit type holds nothing there.)
 // With lo > 0 an infinity stays one. DIVIDE, the division instruction, is for the rest: bf16
 // stores, and divisors whose parts would leave the normal floats. On 16384 tokens of bf16
-// it takes 75.4 us against 65.1 with the products; in one kernel with them its registers
+// it takes 74.6 us against 64.5 with the products; in one kernel with them its registers
 // alone cost 6%, so that it has kernels of its own.
 template <int KV, bool DIVIDE>
 __device__ __forceinline__ Quad over(const Quad &x, const Divisor &s)

@@ -607,7 +607,7 @@ class PagePool:
         d.row_stride, d.num_rows, d.num_pages, d.page_size = table.shape[1], table.shape[0], refs.shape[0], self.page_size
         d.workspace, d.workspace_bytes, d.status = self._workspace.data_ptr(), size.value, self._status.data_ptr()
         self._desc = d
-        self._home = _stream_handle()  # the stream whose memory this is
+        self._streams = {_stream_handle()}  # whose memory this is, and those that it is recorded on
 
     @classmethod
     def empty(cls, *, num_rows: int, max_pages: int, num_pages: int, page_size: int, device="cuda") -> "PagePool":
@@ -618,9 +618,10 @@ class PagePool:
     def _used_on(self, stream) -> int:
         """The handle of a call's stream, which from now on may be using the pool's memory."""
         handle = _stream_handle(stream)
-        if handle != self._home:
+        if handle not in self._streams:  # (a tensor stays recorded)
             _on(torch.cuda.current_stream() if stream is None else stream, self.table, self.lens, self.refs,
                 self._workspace, self._status)
+            self._streams.add(handle)
         return handle
 
     def _index(self, *tensors):

@@ -707,8 +707,9 @@ int take_pool(const char *call, const pkv_page_pool *pool, PoolParams &p)
         return refuse(PKV_ERR_INVALID_ARG, call, "pool is NULL");
     if (pool->num_rows < 0 || pool->num_pages < 0 || pool->row_stride < 0 || pool->page_size <= 0)
         return refuse(PKV_ERR_INVALID_ARG, call, "negative size, or page_size <= 0");
-    if (pool->row_stride > INT32_MAX || pool->num_pages > INT32_MAX - 4096)
-        return refuse(PKV_ERR_UNSUPPORTED, call, "a row or a pool of about 2^31 pages or more");
+    // (segments and loop steps of the scans are rounded up in 32 bits)
+    if (pool->row_stride > INT32_MAX || pool->num_pages > INT32_MAX - 4096 || pool->num_rows > INT32_MAX - 4096)
+        return refuse(PKV_ERR_UNSUPPORTED, call, "a row or a pool of about 2^31 pages, or as many rows");
     if ((pool->num_rows > 0 && (!pool->lens || (pool->row_stride > 0 && !pool->table))) ||
         (pool->num_pages > 0 && !pool->refs) || !pool->status)
         return refuse(PKV_ERR_INVALID_ARG, call, "table, lens, refs and status are required");

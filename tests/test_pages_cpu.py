@@ -82,6 +82,18 @@ def test_bad_pools(lib, over, status):
     assert lib.pkv_pages_compact(ok, d, p, p, 1, p, None) == status
 
 
+def test_pools_of_about_2_31_rows_or_pages_are_refused(lib):
+    """Where a scan's rounded-up segments would pass 32 bits."""
+    p = ctypes.c_void_p(0x1000)
+    for over in (dict(num_rows=2 ** 31 - 1), dict(num_rows=2 ** 31 - 4096), dict(num_pages=2 ** 31 - 4095)):
+        d = _pool(workspace_bytes=1 << 40, **over)
+        for n in (1, 4):
+            assert lib.pkv_pages_extend(d, p, p, n, None, 0, None) == pkv.PKV_ERR_UNSUPPORTED, over
+            assert lib.pkv_pages_fork(d, p, p, n, p, p, None) == pkv.PKV_ERR_UNSUPPORTED
+            assert lib.pkv_pages_free(d, p, n, None) == pkv.PKV_ERR_UNSUPPORTED
+        assert lib.pkv_pages_compact(d, d, p, p, 1, p, None) == pkv.PKV_ERR_UNSUPPORTED
+
+
 def test_bad_calls(lib):
     d, p, odd = _pool(), ctypes.c_void_p(0x1000), ctypes.c_void_p(0x1002)
     bad = pkv.PKV_ERR_INVALID_ARG

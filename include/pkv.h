@@ -226,10 +226,12 @@ PKV_API int pkv_plan_create_capturable(pkv_plan **out, const pkv_plan_desc *desc
  * With no window, or num_sinks = 0, the plan is that of pkv_plan_create /
  * pkv_plan_create_capturable. Every kind, head_dim, page size and kv_dtype is supported,
  * and pkv_run, pkv_plan_update (which keeps num_sinks) and the other calls take the plan
- * as any other. Pages of a request that hold neither one of its first num_sinks keys nor
- * a key at or after p - window_left of one of its queries are not read, so their entries
- * in kv_indices may be anything (pages given back to a pool, say); a decode split over
- * several CTAs counts its splits over the visible keys.
+ * as any other; pkv_decode_noalloc, which takes no plan, has no sinks. Pages of a request
+ * that hold neither one of its first num_sinks keys nor a key at or after p - window_left
+ * of one of its queries are not read, so their entries in kv_indices may be anything: a
+ * caller that manages pages itself may have given them away (pkv_pages_free below gives
+ * back whole rows only). A decode split over several CTAs counts its splits over the
+ * visible keys.
  * Prefill weighs the V rows of the pages it reads with 0 where a query does not see them,
  * with and without sinks, so that those of the request's keys must be finite there; K
  * may hold anything, as may both for decode.
@@ -288,9 +290,10 @@ PKV_API int pkv_plan_destroy(pkv_plan *plan);
 PKV_API int pkv_plan_get_info(const pkv_plan *plan, pkv_plan_info *info);
 
 /*
- * Read and clear the plan's device status word: synchronises the device, stores
- * PKV_OK or PKV_ERR_DEVICE_BOUNDS / PKV_ERR_TIMEOUT recorded by earlier runs in
- * *status, and returns PKV_OK (or PKV_ERR_CUDA if the read itself failed).
+ * Read and clear the plan's device status word: synchronises the device (again after the
+ * clearing, so that nothing recorded later is lost), stores PKV_OK or
+ * PKV_ERR_DEVICE_BOUNDS / PKV_ERR_TIMEOUT recorded by earlier runs in *status, and returns
+ * PKV_OK (or PKV_ERR_CUDA if the read itself failed).
  */
 PKV_API int pkv_plan_device_status(const pkv_plan *plan, int32_t *status);
 
@@ -305,7 +308,7 @@ PKV_API int pkv_plan_set_timing_events(pkv_plan *plan, void *ev_begin, void *ev_
 /*
  * pkv_decode_noalloc: the decode of pkv_plan_create + pkv_run (desc->kind must be
  * PKV_DECODE, desc->kv_dtype PKV_BF16, else PKV_ERR_UNSUPPORTED; same arguments,
- * layouts and results) in one call that allocates no
+ * layouts and results; no sinks) in one call that allocates no
  * device memory: no cudaMalloc, cudaFree or allocating library routine. The pages
  * have no counterpart to it. It is for callers that cannot allocate: serving
  * processes whose memory pool already holds the device memory and forbids further
@@ -393,7 +396,9 @@ typedef struct pkv_append_desc {
  *     (a, b) -> (a cos - b sin, b cos + a sin)  for the pairs of the first rotary_dim columns
  *     k_cache[slot] = y / k_scale, v_cache[slot] = v / v_scale   (pkv_run multiplies them back)
  * All in fp32 from the bf16 inputs, each result rounded once; 8-bit stores round to
- * nearest even and keep to the format's finite range.
+ * nearest even and keep to the format's finite range. The quotients are the fp32 ones (over
+ * an 8-bit cache, where one lies within a relative 2^-47 of the middle between two floats,
+ * either of them), so that v is stored as v / v_scale rounded to fp32, then to the cache's type.
  * DEVICE pointers: q [num_tokens, num_qo_heads, head_dim], k and v [num_tokens,
  * num_kv_heads, head_dim] bf16 with the descriptor's token strides; q_weight, k_weight
  * [head_dim] bf16, or NULL: that tensor is not normalised; cos_sin [max_position,
@@ -469,7 +474,8 @@ PKV_API int pkv_pages_fork(const pkv_page_pool *pool, const int32_t *parents, co
                            int32_t *src, int32_t *dst, void *stream);
 
 /*
- * pkv_pages_free: the rows become empty; pages that no other row names are free again. A
+ * pkv_pages_free: the rows become empty; pages that no other row names are free again (a
+ * row's pages that a window has passed stay its own: none is given back before the rest). A
  * row named twice is freed once; one out of range, or whose length is not one, is recorded
  * and skipped.
  */

@@ -248,15 +248,20 @@ def _within(stream):
 
 
 def _made(stream, make, *args, **kw):
-    """A call's result, made by make(...). On an explicit stream it is that stream's own memory
-    (what the current stream has just given up may still be in use there), and the current
-    stream, on which the caller goes on with it, is recorded."""
-    if stream is None:
-        return make(*args, **kw)
+    """The result of a call on an explicit stream, made by make(...): that stream's own memory
+    (what the current stream has just given up may still be in use there), with the current
+    stream, on which the caller goes on with it, recorded."""
     with _within(stream):
         t = make(*args, **kw)
     _on(torch.cuda.current_stream(), t)
     return t
+
+
+def _empty(stream, shape, dtype, device):
+    """Memory for the result of a call, on whatever stream."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    return _made(stream, torch.empty, shape, dtype=dtype, device=device)
 
 
 def _ptrs(*tensors):
@@ -408,9 +413,10 @@ class Plan:
             if t.dtype != dt or not t.is_cuda or not t.is_contiguous():
                 raise ValueError(f"{name} must be a contiguous CUDA {dt} tensor")
         if out is None:
-            out = _made(stream, torch.empty_like, q)
+            out = torch.empty_like(q) if stream is None else _made(stream, torch.empty_like, q)
         if return_lse and lse is None:
-            lse = _made(stream, torch.empty, q.shape[:2], dtype=torch.float32, device=q.device)
+            lse = (torch.empty(q.shape[0], q.shape[1], dtype=torch.float32, device=q.device) if stream is None else
+                   _made(stream, torch.empty, q.shape[:2], dtype=torch.float32, device=q.device))
         _check(self._lib.pkv_run(self._handle, _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(out),
                                  _ptr(lse), _stream_handle(stream)), "pkv_run")
         return (out, lse) if (return_lse or lse is not None) else out
@@ -453,12 +459,12 @@ def build_kv_indices(req_to_token: torch.Tensor, req_pool_indices: torch.Tensor,
             raise ValueError(f"{name} must be a contiguous CUDA int32 tensor")
     B = kv_lens.numel()
     if kv_indptr is None:
-        kv_indptr = _made(stream, torch.empty, (B + 1,), dtype=torch.int32, device=kv_lens.device)
+        kv_indptr = _empty(stream, (B + 1,), torch.int32, kv_lens.device)
     if kv_indices is None:
         if capacity is None:
             with _within(stream):  # behind whatever writes them there
                 capacity = int(kv_lens.clamp(min=0).sum().item())
-        kv_indices = _made(stream, torch.empty, (max(1, capacity),), dtype=torch.int32, device=kv_lens.device)
+        kv_indices = _empty(stream, (max(1, capacity),), torch.int32, kv_lens.device)
     cap = kv_indices.numel() if capacity is None else min(int(capacity), kv_indices.numel())
     _check(lib.pkv_build_kv_indices(_ptr(req_to_token), req_to_token.shape[0], req_to_token.shape[1],
                                     _ptr(req_pool_indices), _ptr(kv_start), _ptr(kv_lens), B, _ptr(loc_map),
@@ -564,10 +570,12 @@ def norm_rope_append(q: Optional[torch.Tensor], k: Optional[torch.Tensor], v: Op
     lib = _lib or load_library()
     # Plain values before the descriptor is looked up: a tensor of one number would be found
     # by its identity, and with it the value that it had in an earlier call.
-    eps, weight_offset, k_scale, v_scale = float(eps), float(weight_offset), float(k_scale), float(v_scale)
-    interleaved = bool(interleaved)
+    if not (eps.__class__ is weight_offset.__class__ is k_scale.__class__ is v_scale.__class__ is float):
+        eps, weight_offset, k_scale, v_scale = float(eps), float(weight_offset), float(k_scale), float(v_scale)
+    if interleaved is not False and interleaved is not True:
+        interleaved = bool(interleaved)
     if q is not None and q_out is None:
-        q_out = _made(stream, torch.empty, q.shape, dtype=torch.bfloat16, device=q.device)
+        q_out = _empty(stream, q.shape, torch.bfloat16, q.device)
     dev = torch.cuda.current_device()
     tensors = (q, k, v, q_weight, k_weight, cos_sin, positions, slots, q_out, k_out, k_cache, v_cache, status)
     key = (dev, eps, weight_offset, interleaved, k_scale, v_scale) + tuple(map(_sig, tensors))
@@ -615,14 +623,12 @@ class PagePool:
         zeros = lambda *shape: torch.zeros(shape, dtype=torch.int32, device=device)  # noqa: E731
         return cls(zeros(num_rows, max_pages), zeros(num_rows), zeros(num_pages), page_size=page_size)
 
-    def _used_on(self, stream) -> int:
-        """The handle of a call's stream, which from now on may be using the pool's memory."""
-        handle = _stream_handle(stream)
+    def _used_on(self, stream, handle):
+        """A call's stream, which from now on may be using the pool's memory."""
         if handle not in self._streams:  # (a tensor stays recorded)
             _on(torch.cuda.current_stream() if stream is None else stream, self.table, self.lens, self.refs,
                 self._workspace, self._status)
             self._streams.add(handle)
-        return handle
 
     def _index(self, *tensors):
         if torch.cuda.current_device() != self._device:
@@ -639,13 +645,16 @@ class PagePool:
         slots are returned, entry after entry."""
         n = self._index(rows, add)
         if slots is None and total is not None:
-            slots = _made(stream, torch.empty, (total,), dtype=torch.int64, device=self.table.device)
+            slots = _empty(stream, (total,), torch.int64, self.table.device)
         elif slots is not None:
             _want(slots, "slots", torch.int64)
             _here(self._device, slots)
+        handle = _stream_handle(stream)
+        if handle not in self._streams:
+            self._used_on(stream, handle)
         _check(self._lib.pkv_pages_extend(self._desc, rows.data_ptr(), add.data_ptr(), n,
                                           None if slots is None else slots.data_ptr(),
-                                          0 if slots is None else slots.numel(), self._used_on(stream)),
+                                          0 if slots is None else slots.numel(), handle),
                "pkv_pages_extend")
         return slots
 
@@ -653,17 +662,25 @@ class PagePool:
              dst: Optional[torch.Tensor] = None, stream=None):
         """children[i], an empty row, becomes a copy of parents[i]: full pages are shared, a
         partly filled last one is new. Returns (src, dst), the pages to copy (or -1)."""
-        src = _made(stream, torch.empty, parents.shape, dtype=torch.int32, device=parents.device) if src is None else src
-        dst = _made(stream, torch.empty, parents.shape, dtype=torch.int32, device=parents.device) if dst is None else dst
+        if src is None:
+            src = torch.empty_like(parents) if stream is None else _made(stream, torch.empty_like, parents)
+        if dst is None:
+            dst = torch.empty_like(parents) if stream is None else _made(stream, torch.empty_like, parents)
         n = self._index(parents, children, src, dst)
+        handle = _stream_handle(stream)
+        if handle not in self._streams:
+            self._used_on(stream, handle)
         _check(self._lib.pkv_pages_fork(self._desc, parents.data_ptr(), children.data_ptr(), n, src.data_ptr(),
-                                        dst.data_ptr(), self._used_on(stream)), "pkv_pages_fork")
+                                        dst.data_ptr(), handle), "pkv_pages_fork")
         return src, dst
 
     def free(self, rows: torch.Tensor, stream=None):
         """The rows become empty; pages that no other row names are free again."""
         n = self._index(rows)
-        _check(self._lib.pkv_pages_free(self._desc, rows.data_ptr(), n, self._used_on(stream)), "pkv_pages_free")
+        handle = _stream_handle(stream)
+        if handle not in self._streams:
+            self._used_on(stream, handle)
+        _check(self._lib.pkv_pages_free(self._desc, rows.data_ptr(), n, handle), "pkv_pages_free")
 
     def compact(self, out: Optional["PagePool"] = None, src: Optional[torch.Tensor] = None,
                 dst: Optional[torch.Tensor] = None, count: Optional[torch.Tensor] = None, stream=None):
@@ -672,19 +689,21 @@ class PagePool:
         device. The caches' pages are the caller's to copy (copy_pages) before the new
         table is used."""
         if src is None:
-            src = _made(stream, torch.empty, (self.refs.shape[0] // 2,), dtype=torch.int32, device=self.table.device)
+            src = _empty(stream, (self.refs.shape[0] // 2,), torch.int32, self.table.device)
         if dst is None:
-            dst = _made(stream, torch.empty, src.shape, dtype=torch.int32, device=self.table.device)
+            dst = _empty(stream, src.shape, torch.int32, self.table.device)
         if count is None:
-            count = _made(stream, torch.empty, (1,), dtype=torch.int32, device=self.table.device)
+            count = _empty(stream, (1,), torch.int32, self.table.device)
         n = self._index(src, dst)
         self._index(count)
         out = self if out is None else out
         if out._device != self._device:
             raise ValueError(f"the pools are on cuda:{self._device} and cuda:{out._device}")
-        out._used_on(stream)
+        handle = _stream_handle(stream)
+        self._used_on(stream, handle)
+        out._used_on(stream, handle)
         _check(self._lib.pkv_pages_compact(self._desc, out._desc, src.data_ptr(), dst.data_ptr(), n,
-                                           count.data_ptr(), self._used_on(stream)), "pkv_pages_compact")
+                                           count.data_ptr(), handle), "pkv_pages_compact")
         return src, dst, count
 
     def device_status(self) -> int:
@@ -743,9 +762,9 @@ def merge_state(v_a: torch.Tensor, s_a: torch.Tensor, v_b: torch.Tensor, s_b: to
     if v_a.shape != v_b.shape or v_a.dim() != 3 or s_a.shape != v_a.shape[:2] or s_b.shape != s_a.shape:
         raise ValueError("shape mismatch")
     if v_out is None:
-        v_out = _made(stream, torch.empty_like, v_a)
+        v_out = torch.empty_like(v_a) if stream is None else _made(stream, torch.empty_like, v_a)
     if s_out is None:
-        s_out = _made(stream, torch.empty_like, s_a)
+        s_out = torch.empty_like(s_a) if stream is None else _made(stream, torch.empty_like, s_a)
     dtype = PKV_BF16 if v_a.dtype == torch.bfloat16 else PKV_F32
     _check(lib.pkv_merge_state(_ptr(v_a), _ptr(s_a), _ptr(v_b), _ptr(s_b), _ptr(v_out), _ptr(s_out),
                                v_a.shape[0], v_a.shape[1], v_a.shape[2], dtype,

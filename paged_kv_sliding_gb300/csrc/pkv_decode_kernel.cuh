@@ -22,8 +22,10 @@
 //     gathers; completion through mbarriers;
 //   compute warp w: tokens [TPW w, TPW w + TPW) of every stage, S = Q K^T and
 //     O += P V with mma.sync m16n8k16 (bf16, or f16 for 8-bit caches, in; fp32
-//     accumulate; rows = the query heads), running its own (m, l, O) without
-//     CTA-wide barriers; the warps' states are merged once at the end. A CTA that
+//     accumulate; rows = the query heads; P is rounded to V's type, since both
+//     operands of an MMA have one: with bf16 the output's error against 64 bits is
+//     0.0022 of its size, 0.0017 being its own rounding, and with f16 0.0017),
+//     running its own (m, l, O) without CTA-wide barriers; the warps' states are merged once at the end. A CTA that
 //     handles one split of a request writes an fp32 partial state; the group's
 //     last CTA to finish (an arrival counter after a memory fence) combines the
 //     partials through their LSE, so no second kernel runs.

@@ -43,9 +43,10 @@
  * ("pkv_run decode" / "pkv_run prefill" for runs), shown by profilers' timelines; with
  * no tool attached the range calls return at once.
  *
- * Threading and streams: a plan may be run from one host thread at a time; all
- * launches are asynchronous on the caller's stream (a cudaStream_t passed as void*,
- * NULL = legacy default stream). pkv_run and pkv_merge_state never synchronise;
+ * Threading and streams: a plan may be run from one host thread at a time, and its runs
+ * (captured graphs of them too) share its workspace, so that they must not overlap on
+ * several streams; all launches are asynchronous on the caller's stream (a cudaStream_t
+ * passed as void*, NULL = legacy default stream). pkv_run and pkv_merge_state never synchronise;
  * pkv_plan_create waits for its own upload and pkv_plan_device_status for the
  * device.
  */

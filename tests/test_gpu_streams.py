@@ -160,3 +160,65 @@ def test_lengths_of_the_page_list_are_read_behind_what_writes_them(pkv):
     indptr, indices = pkv.build_kv_indices(table, rows, start, lens, stream=side)
     side.synchronize()
     assert indptr.tolist() == [0, 4, 9] and indices.tolist() == [30, 31, 32, 33, 2, 3, 4, 5, 6]
+
+
+def test_captured_calls_behind_other_nodes_and_other_streams(pkv):
+    """In a graph, each call right behind a memset, a copy and the join of two streams (the
+    kernels' early start is meant for a kernel ahead of them alone); replayed over changing
+    contents, against the same calls one by one."""
+    hkv, d, P, pages = 2, 64, 4, 60
+    w = inputs.batch_decode(127, batch=8).to("cuda")
+    plan = pkv.plan_for(w, num_sinks=4)
+    pool = pkv.PagePool.empty(num_rows=6, max_pages=20, num_pages=pages, page_size=P)
+    rows, add, child = _i32(0, 1, 2), _i32(9, 3, 14), _i32(4)
+    k = torch.randn(26, hkv, d, device="cuda").to(torch.bfloat16)
+    q, fresh = w.q.clone(), w.q.clone()
+    caches = [torch.zeros(pages, P, hkv, d, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    slots = torch.zeros(26, dtype=torch.int64, device="cuda")
+    src, dst = torch.zeros_like(child), torch.zeros_like(child)
+    out, lse = torch.zeros_like(q), torch.zeros(q.shape[:2], device="cuda")
+    side = torch.cuda.Stream()
+
+    def step():
+        now = torch.cuda.current_stream()
+        for x in (pool.table, pool.lens, pool.refs):
+            x.zero_()
+        slots.zero_()  # a memset ahead of the ranking
+        pool.extend(rows, add, slots=slots)
+        side.wait_stream(now)
+        with torch.cuda.stream(side):  # beside the append
+            q.copy_(fresh)  # a copy ahead of the attention
+            plan.run(q, w.k_cache, w.v_cache, out, lse)
+            src.fill_(5)
+        pkv.norm_rope_append(None, k, k, slots=slots, k_cache=caches[0], v_cache=caches[1])
+        now.wait_stream(side)
+        pool.fork(rows[2:], child, src=src, dst=dst)  # behind both streams
+        side.wait_stream(now)
+        with torch.cuda.stream(side):
+            pkv.copy_pages(*caches, src, dst)
+        pkv.norm_rope_append(q, None, q_out=q)
+        now.wait_stream(side)
+        pool.free(rows[:1])
+
+    state = (pool.table, pool.lens, pool.refs, *caches, slots, src, dst, out, lse, q)
+    step()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    for i in range(20):
+        k.copy_(torch.randn(k.shape, device="cuda"))
+        fresh.copy_(torch.randn(q.shape, device="cuda"))
+        add.copy_(_i32(*((9, 3, 14), (1, 20, 5), (4, 4, 18))[i % 3]))
+        step()
+        torch.cuda.synchronize()
+        want = [x.clone() for x in state]
+        for x in state[3:]:
+            x.zero_()
+        for c, old in zip(caches, want[3:5]):
+            c.copy_(old)
+        g.replay()
+        torch.cuda.synchronize()
+        assert pool.device_status() == plan.device_status() == pkv.PKV_OK
+        assert all(torch.equal(x, y) for x, y in zip(state, want)), i
+    assert pool.lens.tolist() == [0, 20, 5, 0, 5, 0]

@@ -474,7 +474,13 @@ PKV_API int pkv_norm_rope_append(const pkv_append_desc *desc, const void *q, con
  * of a head's row y, in fp32:
  *     s = max |y| / (6 k_scale), rounded to E4M3 (nearest even, 448 at most)
  *     value = y / (s * k_scale), rounded to E2M1 (nearest even, 6 at most); 0 where s is 0
- * so that a block's largest value is about its largest code. Of a slot that is skipped
+ * so that a block's largest value is about its largest code. A K that is normalised or rotated is
+ * an fp32 number before that, and a value, or a block's largest, next to the middle of two codes
+ * takes that number's code. It is the one that the formulas above give with each operation rounded
+ * to fp32 by itself: the squares added up (head_dim 64 and 128: columns 32 apart in turn, then
+ * neighbours, pairs of them and so on; 256: the two halves, four neighbours in turn, then
+ * neighbouring fours, pairs of them and so on), their mean plus eps, its reciprocal root
+ * (rsqrtf), two products, and the rotation's two products and their sum. Of a slot that is skipped
  * neither values nor scales are written; rows that share a slot may leave parts of either, with
  * scales of the other. With any other kv_dtype both scales are NULL and the call is
  * pkv_norm_rope_append.

@@ -11,7 +11,10 @@
 // store takes the nearest finite value. A 4-bit cache (e2m1) has an e4m3 scale for every 16
 // columns of a row beside it:
 //   s = e4m3(max |y| / (6 scale)),  u = s scale,  cache[slot] = e2m1(y / u)  (0 where u = 0)
-// with u and both quotients in fp32.
+// with u and both quotients in fp32. A code is a step function of y, so that a last bit of y can
+// move a value by a third of itself. Into such a cache y is therefore what the formulas give with
+// every operation rounded to fp32 by itself (no fused rotation) and the squares summed in the
+// order of `square_sum`: a program of elementwise fp32 operations finds the same codes.
 //
 // Bound by memory: every row is read once and written once, and the pass does about one
 // flop a byte; what stands in its way is the number of instructions, so that
@@ -25,13 +28,15 @@
 // SMs, 2.1 us), HPG = 4 otherwise. Measured on 16384 tokens x 48 heads of 128, bf16: 64.5 us
 // = 6.37 TB/s, 0.94 of the copy rate; 8191 tokens of 8 + 2 x 4 heads of 256 into E4M3 22.5 us
 // (with products by one rounded reciprocal 22.15; eight heads to a group, measured with
-// those, 62 and 23.4 us: on the second they stay half empty). Into 4-bit caches the first takes 70.7 us
-// for 354 MB (5.0 TB/s, 0.74 of the copy rate) and the second 25.4: the blocks' shuffles, codes and
-// quotients are a third of the instructions. With division instructions for the quotients, whose
-// registers (72, against 60) kept warps out, 76 us.
+// those, 62 and 23.4 us: on the second they stay half empty). Into 4-bit caches the first takes 74.5 us
+// for 354 MB (4.75 TB/s, 0.70 of the copy rate) and the second 26.0: the blocks' shuffles, codes and
+// quotients are a third of the instructions, and registers keep warps out. With the registers of 9
+// blocks an SM (kFp4Blocks) 74.5 us, of 8 76.2, of 10 79.1, as the compiler likes (7) 80.3. The
+// sums of `square_sum` and k's unfused rotation are 3.4 us of it (71.1 and 25.3 without).
 #include <cfloat>
 #include <cmath>
 #include <string>
+#include <type_traits>
 
 #include <cuda_fp8.h>
 
@@ -43,6 +48,7 @@ namespace pkv {
 namespace {
 
 constexpr int kThreads = 128;
+constexpr int kFp4Blocks = 9;  // of an SM, 4-bit caches
 
 // What a value is divided by: the divisor and its reciprocal in two parts, hi + lo, lo > 0, or
 // hi alone (lo = 0) where that is exact.
@@ -131,6 +137,24 @@ __device__ __forceinline__ float product(float a, float b)
     return r;
 }
 
+// a + b, subnormals kept, and never fused with a product before it.
+__device__ __forceinline__ float sum(float a, float b)
+{
+    float r;
+    asm("add.rn.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+// a b + c d. PLAIN: each product rounded by itself (one number at a time: of packed pairs the
+// assembler fuses product and sum, rounding modifiers or not, as the results show).
+template <bool PLAIN>
+__device__ __forceinline__ float2 sum_of_products(float2 a, float2 b, float2 c, float2 d)
+{
+    if (!PLAIN)
+        return fma2(a, b, mul2(c, d));
+    return make_float2(sum(product(a.x, b.x), product(c.x, d.x)), sum(product(a.y, b.y), product(c.y, d.y)));
+}
+
 // x / s. A product with the rounded reciprocal alone is off by up to 1.5 steps of fp32, which
 // moves a quotient halfway between two stored values (bf16 inputs give many) to either
 // side. x hi + x lo, the small product rounded and the sum of a fused multiply-add (the
@@ -153,6 +177,43 @@ __device__ __forceinline__ Quad over(const Quad &x, const Divisor &s)
     const float2 hi = make_float2(s.hi, s.hi);
     const Quad low = scaled(x, s.lo);
     return {fma2(x.a, hi, low.a), fma2(x.b, hi, low.b)};
+}
+
+// The sum of a row's D squares in a fixed order, whatever columns the lanes hold for the rotation
+// (the row is read again, from L1). d 64 and 128: of columns 32 apart in turn, then of neighbours,
+// pairs of neighbours and so on; d 256: of the two halves, of four neighbours in turn, then of
+// neighbouring fours, pairs of these and so on. The square of a bf16 value is exact in fp32, so that
+// a fused multiply-add rounds as the addition does. (Lane l of a row's D / 8; all lanes come here.)
+template <int D>
+__device__ __forceinline__ float square_sum(const uint16_t *row, int l, bool there)
+{
+    float s;
+    if (D == 128) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            w[i] = there ? *reinterpret_cast<const uint32_t *>(row + 2 * l + 32 * i) : 0u;
+        float2 x = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 y = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+            x = fma2(y, y, x);
+        }
+        s = x.x + x.y;
+    } else {
+        uint2 a = make_uint2(0u, 0u), b = a;
+        if (there) {
+            a = *reinterpret_cast<const uint2 *>(row + 4 * l);
+            b = *reinterpret_cast<const uint2 *>(row + D / 2 + 4 * l);
+        }
+        const Quad x = widen(a), y = widen(b);
+        const float2 u = fma2(y.a, y.a, mul2(x.a, x.a)), v = fma2(y.b, y.b, mul2(x.b, x.b));
+        s = D == 64 ? (u.x + u.y) + (v.x + v.y) : ((u.x + u.y) + v.x) + v.y;
+    }
+#pragma unroll
+    for (int o = 1; o < D / 8; o <<= 1)
+        s += __shfl_xor_sync(0xffffffffu, s, o);
+    return s;
 }
 
 // The lane's two pieces of a row, at columns c0 and c1; ONE: c1 = c0 + 4, one access.
@@ -307,9 +368,10 @@ __device__ __forceinline__ void store_blocks(void *base, uint8_t *scales, int64_
 }
 
 template <int D, int HPG, int KV, bool INTERLEAVED, bool DIVIDE>
-__global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p)
+__global__ void __launch_bounds__(kThreads, KV == PKV_FP4_E2M1 ? kFp4Blocks : 1) append_kernel(const AppendParams p)
 {
     constexpr int G = D / 8;  // lanes of a row
+    constexpr bool kPlain = KV == PKV_FP4_E2M1;  // k: every fp32 operation rounded by itself
     grid_dependency_wait();
     grid_launch_dependents();
     // The block's tensor and heads: q's chunks first, then k's, then v's.
@@ -365,6 +427,13 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p)
         }
         return;
     }
+    const uint16_t *weight = is_q ? p.q_weight : p.k_weight;
+    float k_squares[HPG] = {};  // (of all heads at once: their loads and shuffles wait together)
+    if (kPlain && !is_q && weight) {
+#pragma unroll
+        for (int j = 0; j < HPG; ++j)
+            k_squares[j] = square_sum<D>(row + j * D, l, there && h0 + j < heads);
+    }
     // cos and sin of the lane's four pairs
     Quad cs{}, sn{};
     if (live && turned) {
@@ -374,7 +443,6 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p)
         cs = {make_float2(x.x, x.y), make_float2(x.z, x.w)};
         sn = {make_float2(y.x, y.y), make_float2(y.z, y.w)};
     }
-    const uint16_t *weight = is_q ? p.q_weight : p.k_weight;
     Quad w0{}, w1{};
     if (weight) {
         w0 = widen(*reinterpret_cast<const uint2 *>(weight + c0));
@@ -388,11 +456,16 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p)
             break;  // the same for every lane
         Quad x0 = widen(raw[j][0]), x1 = widen(raw[j][1]);
         if (weight) {
-            float2 s2 = fma2(x1.b, x1.b, fma2(x1.a, x1.a, fma2(x0.b, x0.b, mul2(x0.a, x0.a))));
-            float ss = s2.x + s2.y;
+            float ss;
+            if (kPlain && !is_q) {
+                ss = k_squares[j];
+            } else {
+                const float2 s2 = fma2(x1.b, x1.b, fma2(x1.a, x1.a, fma2(x0.b, x0.b, mul2(x0.a, x0.a))));
+                ss = s2.x + s2.y;
 #pragma unroll
-            for (int o = G / 2; o >= 1; o >>= 1)
-                ss += __shfl_xor_sync(0xffffffffu, ss, o);
+                for (int o = G / 2; o >= 1; o >>= 1)
+                    ss += __shfl_xor_sync(0xffffffffu, ss, o);
+            }
             const float r = rsqrtf(ss * (1.f / D) + p.eps);
             x0 = scaled(x0, r);
             x1 = scaled(x1, r);
@@ -409,8 +482,16 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p)
                 b = {make_float2(x0.a.y, x0.b.y), make_float2(x1.a.y, x1.b.y)};
             }
             const Quad neg = scaled(sn, -1.f);
-            const Quad ra{fma2(a.a, cs.a, mul2(b.a, neg.a)), fma2(a.b, cs.b, mul2(b.b, neg.b))};
-            const Quad rb{fma2(b.a, cs.a, mul2(a.a, sn.a)), fma2(b.b, cs.b, mul2(a.b, sn.b))};
+            Quad ra, rb;
+            auto turn = [&](auto plain) {
+                constexpr bool P = decltype(plain)::value;
+                ra = {sum_of_products<P>(a.a, cs.a, b.a, neg.a), sum_of_products<P>(a.b, cs.b, b.b, neg.b)};
+                rb = {sum_of_products<P>(b.a, cs.a, a.a, sn.a), sum_of_products<P>(b.b, cs.b, a.b, sn.b)};
+            };
+            if (kPlain && !is_q)
+                turn(std::true_type{});
+            else
+                turn(std::false_type{});
             if (INTERLEAVED) {
                 x0 = {make_float2(ra.a.x, rb.a.x), make_float2(ra.a.y, rb.a.y)};
                 x1 = {make_float2(ra.b.x, rb.b.x), make_float2(ra.b.y, rb.b.y)};

@@ -368,7 +368,7 @@ __device__ __forceinline__ void store_blocks(void *base, uint8_t *scales, int64_
 }
 
 template <int D, int HPG, int KV, bool INTERLEAVED, bool DIVIDE>
-__global__ void __launch_bounds__(kThreads, KV == PKV_FP4_E2M1 ? kFp4Blocks : 1) append_kernel(const AppendParams p)
+__global__ void __launch_bounds__(kThreads, KV == PKV_FP4_E2M1 && HPG > 1 ? kFp4Blocks : 0) append_kernel(const AppendParams p)
 {
     constexpr int G = D / 8;  // lanes of a row
     constexpr bool kPlain = KV == PKV_FP4_E2M1;  // k: every fp32 operation rounded by itself

@@ -474,7 +474,9 @@ PKV_API int pkv_norm_rope_append(const pkv_append_desc *desc, const void *q, con
  * of a head's row y, in fp32:
  *     s = max |y| / (6 k_scale), rounded to E4M3 (nearest even, 448 at most)
  *     value = y / (s * k_scale), rounded to E2M1 (nearest even, 6 at most); 0 where s is 0
- * so that a block's largest value is about its largest code. A K that is normalised or rotated is
+ * so that a block's largest value is about its largest code. A block with an infinity has the
+ * scale 448 and the infinity its largest code; one with a NaN has a NaN for its scale, which is
+ * what all of its values then are. A K that is normalised or rotated is
  * an fp32 number before that, and a value, or a block's largest, next to the middle of two codes
  * takes that number's code. It is the one that the formulas above give with each operation rounded
  * to fp32 by itself: the squares added up (head_dim 64 and 128: columns 32 apart in turn, then

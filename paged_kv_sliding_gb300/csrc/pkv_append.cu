@@ -258,14 +258,23 @@ __device__ __forceinline__ void store_row(void *base, int64_t at, int c0, int c1
     }
 }
 
+// The larger of two, a NaN if either is one.
+__device__ __forceinline__ float larger(float a, float b)
+{
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
 __device__ __forceinline__ float largest(const Quad &x)
 {
-    return fmaxf(fmaxf(fabsf(x.a.x), fabsf(x.a.y)), fmaxf(fabsf(x.b.x), fabsf(x.b.y)));
+    return larger(larger(fabsf(x.a.x), fabsf(x.a.y)), larger(fabsf(x.b.x), fabsf(x.b.y)));
 }
 
 // The e4m3 code of a block whose largest value is `amax`. The quotient by the two parts of the
 // reciprocal, as in `over`, takes the same code as the exact one: that is halfway between two
-// codes or a relative 2^-29 away from there, 6 scale times such a middle having 29 bits.
+// codes or a relative 2^-29 away from there, 6 scale times such a middle having 29 bits. Of a block
+// with a NaN it is the type's NaN.
 __device__ __forceinline__ uint32_t block_code(float amax, const BlockDivisor &s6)
 {
     const float x = product(amax, s6.shift);
@@ -278,10 +287,10 @@ __device__ __forceinline__ uint32_t block_code(float amax, const BlockDivisor &s
 // 2^-27 away from there. Values of bf16 often lie halfway, where a product with r alone would
 // go to either side. `plain`: the values are finite, and u is in [2^-64, 2^64], so that
 // reciprocal and remainder are normal floats. Otherwise both are moved by a power of two, and a
-// value beyond 8 u, whose code is the largest one's (NaN too), to there.
+// value beyond 8 u, whose code is the largest one's, to there.
 __device__ __forceinline__ uint32_t e2m1x4(Quad x, float u, bool plain)
 {
-    if (u == 0.f)
+    if (!(u > 0.f))  // (or a NaN: the block's scale says it)
         return 0;
     float nu = -u;
     if (!plain) {
@@ -316,9 +325,9 @@ __device__ __forceinline__ void store_blocks(void *base, uint8_t *scales, int64_
     constexpr int G = D / 8;
     float m0 = largest(x0), m1 = largest(x1);
     if (ONE || !split)
-        m0 = m1 = fmaxf(m0, m1);
-    m0 = fmaxf(m0, __shfl_xor_sync(mask, m0, 1, G));
-    m1 = ONE ? m0 : fmaxf(m1, __shfl_xor_sync(mask, m1, 1, G));
+        m0 = m1 = larger(m0, m1);
+    m0 = larger(m0, __shfl_xor_sync(mask, m0, 1, G));
+    m1 = ONE ? m0 : larger(m1, __shfl_xor_sync(mask, m1, 1, G));
     if (!ONE) {
         // Split pairs: the rotated half row is rotary_dim / 8 quads in the first pieces of as many
         // lanes, then the same in their second pieces. Blocks are lanes 4i .. 4i + 3 of a piece,
@@ -339,8 +348,8 @@ __device__ __forceinline__ void store_blocks(void *base, uint8_t *scales, int64_
                 b = last;
         }
         if (split) {
-            m0 = fmaxf(m0, a);
-            m1 = fmaxf(m1, b);
+            m0 = larger(m0, a);
+            m1 = larger(m1, b);
         }
     }
     const uint32_t s0 = block_code(m0, s6);

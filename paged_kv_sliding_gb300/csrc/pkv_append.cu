@@ -278,7 +278,8 @@ __device__ __forceinline__ float largest(const Quad &x)
 __device__ __forceinline__ uint32_t block_code(float amax, const BlockDivisor &s6)
 {
     const float x = product(amax, s6.shift);
-    return __nv_cvt_float_to_fp8(fmaf(x, s6.hi, x * s6.lo), __NV_SATFINITE, __NV_E4M3);
+    const float low = s6.lo == 0.f ? 0.f : x * s6.lo;  // (hi is exact: an infinity stays one)
+    return __nv_cvt_float_to_fp8(fmaf(x, s6.hi, low), __NV_SATFINITE, __NV_E4M3);
 }
 
 // Four values over u as e2m1, in 16 bits. The quotient is x r with r the reciprocal to within

@@ -286,8 +286,8 @@ __device__ __forceinline__ uint32_t block_code(float amax, const BlockDivisor &s
 // 2^-22, corrected by its remainder e = x - x r u (one fused multiply-add): off by a relative
 // 2^-43 before its one rounding, where a quotient that is not halfway between two codes is
 // 2^-27 away from there. Values of bf16 often lie halfway, where a product with r alone would
-// go to either side. `plain`: the values are finite, and u is in [2^-64, 2^64], so that
-// reciprocal and remainder are normal floats. Otherwise both are moved by a power of two, and a
+// go to either side. `plain`: u is in [2^-64, 2^64] and no value is beyond 2^60 u, so that
+// reciprocal, quotient and remainder are finite. (A block whose scale is 448 may hold larger ones.) Otherwise both are moved by a power of two, and a
 // value beyond 8 u, whose code is the largest one's, to there.
 __device__ __forceinline__ uint32_t e2m1x4(Quad x, float u, bool plain)
 {
@@ -359,7 +359,7 @@ __device__ __forceinline__ void store_blocks(void *base, uint8_t *scales, int64_
         return product(__half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)code, __NV_E4M3))), scale);
     };
     const float u0 = unit(s0), u1 = ONE ? u0 : unit(s1);
-    auto plain = [](float u, float m) { return u >= 0x1p-64f && u <= 0x1p64f && m <= FLT_MAX; };
+    auto plain = [](float u, float m) { return u >= 0x1p-64f && u <= 0x1p64f && m <= 0x1p60f * u; };
     const uint32_t w0 = e2m1x4(x0, u0, plain(u0, m0)), w1 = e2m1x4(x1, u1, plain(u1, m1));
     uint8_t *row = static_cast<uint8_t *>(base) + at * (D / 2);
     uint8_t *scale_row = scales + at * (D / 16);

@@ -101,7 +101,8 @@ typedef enum pkv_dtype {
                          byte with the even column in the low half, [num_pages, page_size, H_kv,
                          d / 2] bytes, and beside each cache an E4M3 scale for every 16 columns
                          of a row, [num_pages, page_size, H_kv, d / 16] bytes:
-                             K = k_scale * block scale * value                              */
+                             K = k_scale * block scale * value
+                         (decode plans: num_pages * page_size below 2^32)                   */
 } pkv_dtype;
 
 /*

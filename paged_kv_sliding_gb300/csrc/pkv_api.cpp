@@ -136,6 +136,9 @@ int validate(const pkv_plan_desc *d, std::vector<HostRequest> &reqs)
     if (d->kv_dtype == PKV_FP4_E2M1 && d->kind != PKV_DECODE)
         return fail(PKV_ERR_UNSUPPORTED,
                     "4-bit caches are for decode plans; prefill reads them through pkv_gather_kv and a ragged plan");
+    if (d->kv_dtype == PKV_FP4_E2M1 && (int64_t)d->num_pages * d->page_size >= (1LL << 32))
+        return fail(PKV_ERR_UNSUPPORTED, "num_pages %d x page_size %d: 4-bit caches of 2^32 rows or more", d->num_pages,
+                    d->page_size);
     if (d->kv_dtype != PKV_BF16 && d->kind == PKV_PREFILL_RAGGED)
         return fail(PKV_ERR_UNSUPPORTED, "8-bit K/V are supported in paged caches only");
     if (!(d->sm_scale == d->sm_scale) || std::isinf(d->sm_scale))

@@ -231,7 +231,7 @@ __global__ void __launch_bounds__(Traits<D, HP, NWH>::kThreads, Traits<D, HP, NW
     if (warp == NW) {
         // ------------------------------------------------------------ producer
         // Rows of a tile are handed out as lane + 32 k (k < KR); a row of the cache, page *
-        // page_size + slot, is below 2^32 - 1 in any cache that fits the device.
+        // page_size + slot, is below 2^32 - 1 (larger caches are refused).
         constexpr int KR = TT / 32;
         constexpr uint32_t kNone = 0xffffffffu;
         const int P = p.page_size, H = p.num_kv_heads;
@@ -333,12 +333,13 @@ __global__ void __launch_bounds__(Traits<D, HP, NWH>::kThreads, Traits<D, HP, NW
                     mbar_arrive_expect_tx(full, (uint32_t)__popc(valid) * rows_box * (TOKEN + (TMA_S ? SL : 0)) * 2);
                 __syncwarp();
                 if (pg >= 0) {
-                    const int x = it.kv_head / HP, row = pg * P + slot0;
-                    tma_load_4d(kb + lane * rows_box * TOKEN, &tm.k, 0, 0, x * NL, row >> 3, full);
-                    tma_load_4d(vb + lane * rows_box * TOKEN, &tm.v, 0, 0, x * NL, row >> 3, full);
+                    // (rows pass 31 bits, their blocks of 8 do not)
+                    const int x = it.kv_head / HP, block = (int)(((uint32_t)pg * (uint32_t)P + (uint32_t)slot0) >> 3);
+                    tma_load_4d(kb + lane * rows_box * TOKEN, &tm.k, 0, 0, x * NL, block, full);
+                    tma_load_4d(vb + lane * rows_box * TOKEN, &tm.v, 0, 0, x * NL, block, full);
                     if (TMA_S) {
-                        tma_load_4d(ksb + lane * rows_box * SL, &tm.ks, 0, 0, x, row >> 3, full);
-                        tma_load_4d(vsb + lane * rows_box * SL, &tm.vs, 0, 0, x, row >> 3, full);
+                        tma_load_4d(ksb + lane * rows_box * SL, &tm.ks, 0, 0, x, block, full);
+                        tma_load_4d(vsb + lane * rows_box * SL, &tm.vs, 0, 0, x, block, full);
                     }
                 }
                 const bool edge = !(ts >= u_lo && ts + TT <= u_hi);

@@ -145,6 +145,18 @@ def test_plans_over_4_bit_caches_are_decode_plans(lib, kind):
     assert lib.pkv_plan_create(ctypes.byref(out), ctypes.byref(d), None) == pkv.PKV_ERR_INVALID_ARG
 
 
+@pytest.mark.parametrize("pages,page,refused", [(1 << 28, 16, True), ((1 << 28) - 1, 16, False), ((1 << 31) - 1, 3, True),
+                                                ((1 << 31) - 1, 1, False)])
+def test_pools_of_2_32_rows_are_refused(lib, pages, page, refused):
+    """The decode counts rows in 32 bits; 2^32 - 1 is no row. (A batch of none: without a GPU what
+    passes the checks fails later.)"""
+    out = ctypes.c_void_p()
+    d = _desc(kind=pkv.PKV_DECODE, num_pages=pages, page_size=page)
+    assert (lib.pkv_plan_create(ctypes.byref(out), ctypes.byref(d), None) == pkv.PKV_ERR_UNSUPPORTED) == refused
+    assert (b"2^32 rows" in lib.pkv_last_error()) == refused
+    lib.pkv_plan_destroy(out)
+
+
 def test_noalloc_decode_refuses_4_bit_caches(lib):
     d = _desc(kind=pkv.PKV_DECODE)
     assert lib.pkv_decode_noalloc(ctypes.byref(d), None, None, None, None, None, None) == pkv.PKV_ERR_UNSUPPORTED

@@ -612,11 +612,21 @@ PKV_API int pkv_pages_compact(const pkv_page_pool *pool, const pkv_page_pool *ou
  * with a negative id are skipped, as are those from *count on (DEVICE; NULL: n); an id
  * beyond the caches is recorded in status (DEVICE or NULL) and its pair skipped. No page
  * may be a dst twice, or a dst and the src of another pair. Asynchronous on `stream`, one
- * launch; capturable. Caches 16-byte aligned.
+ * launch; capturable. Caches 16-byte aligned. (4-bit caches: pkv_copy_pages_blocks.)
  */
 PKV_API int pkv_copy_pages(void *k_cache, void *v_cache, int32_t num_layers, int64_t layer_bytes, int32_t num_pages,
                            int64_t page_bytes, const int32_t *src, const int32_t *dst, int32_t n, const int32_t *count,
                            int32_t *status, void *stream);
+
+/*
+ * pkv_copy_pages_blocks: the same of a 4-bit cache with its block scales, whose pages have
+ * scale_page_bytes (page_size * H_kv * head_dim / 16, a multiple of 4) and whose layers are
+ * scale_layer_bytes apart (a multiple of 4). All four arrays 16-byte aligned; two launches.
+ */
+PKV_API int pkv_copy_pages_blocks(void *k_cache, void *v_cache, void *k_block_scales, void *v_block_scales,
+                                  int32_t num_layers, int64_t layer_bytes, int64_t scale_layer_bytes, int32_t num_pages,
+                                  int64_t page_bytes, int64_t scale_page_bytes, const int32_t *src, const int32_t *dst,
+                                  int32_t n, const int32_t *count, int32_t *status, void *stream);
 
 /* PKV_ABI_VERSION of the loaded library. */
 PKV_API int pkv_abi_version(void);

@@ -619,7 +619,8 @@ __global__ void __launch_bounds__(kRewriteThreads) rewrite_kernel(const PoolPara
     }
 }
 
-// Whole pages of K and V, of every layer, in 16-byte granules: a CTA takes tiles of
+// Whole pages of K and V, of every layer, in granules of 16 bytes, or of 4 where the block scales
+// of a page are not whole 16 bytes (5 tokens of 2 heads of 64 have 40): a CTA takes tiles of
 // kTile granules of one cache, each thread kUnroll of them, all loaded before the first
 // is stored. Bound by HBM.
 constexpr int kCopyThreads = 256, kUnroll = 8, kTile = kCopyThreads * kUnroll;
@@ -634,8 +635,10 @@ struct CopyParams {
     int32_t *status;
 };
 
+template <typename Granule>
 __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const CopyParams p)
 {
+    constexpr int W = sizeof(Granule);
     grid_dependency_wait();
     grid_launch_dependents();
     const int n = p.count ? max(0, min(p.n, *p.count)) : p.n;
@@ -645,7 +648,7 @@ __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const CopyParams p)
         uint8_t *cache = (which & 1 ? p.v : p.k) + (which >> 1) * p.layer_bytes;
         const long long g0 = (tile - which * per_cache) * kTile;
         const int pair0 = (int)(g0 / p.granules), rest = (int)(g0 - (long long)pair0 * p.granules);
-        uint4 x[kUnroll];
+        Granule x[kUnroll];
         int64_t to[kUnroll];
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
@@ -659,9 +662,9 @@ __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const CopyParams p)
                     if (p.status)
                         record_status(p.status, PKV_ERR_DEVICE_BOUNDS);
                 } else if (a >= 0 && z >= 0) {
-                    const int64_t in = (int64_t)(g - (unsigned)step * (unsigned)p.granules) * 16;
-                    const int64_t page = (int64_t)p.granules * 16;
-                    x[u] = *reinterpret_cast<const uint4 *>(cache + a * page + in);
+                    const int64_t in = (int64_t)(g - (unsigned)step * (unsigned)p.granules) * W;
+                    const int64_t page = (int64_t)p.granules * W;
+                    x[u] = *reinterpret_cast<const Granule *>(cache + a * page + in);
                     to[u] = z * page + in;
                 }
             }
@@ -669,7 +672,7 @@ __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const CopyParams p)
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u)
             if (to[u] >= 0)
-                *reinterpret_cast<uint4 *>(cache + to[u]) = x[u];
+                *reinterpret_cast<Granule *>(cache + to[u]) = x[u];
     }
 }
 
@@ -772,6 +775,54 @@ cudaError_t launch(void (*kernel)(Params...), int grid, int threads, int cluster
 int launched(const char *call, cudaError_t ce)
 {
     return ce == cudaSuccess ? PKV_OK : refuse(PKV_ERR_CUDA, call, cudaGetErrorString(ce));
+}
+
+// The checks of a copy in granules of a type, and its parameters.
+template <typename Granule>
+int take_copy(const char *call, void *k, void *v, int32_t num_layers, int64_t layer_bytes, int32_t num_pages,
+              int64_t page_bytes, const int32_t *src, const int32_t *dst, int32_t n, const int32_t *count, int32_t *status,
+              CopyParams &p)
+{
+    constexpr int W = sizeof(Granule);
+    p = CopyParams{};
+    if (n < 0 || num_layers < 0 || num_pages < 0 || page_bytes < 0 || layer_bytes < 0)
+        return refuse(PKV_ERR_INVALID_ARG, call, "negative size");
+    if (page_bytes % W || layer_bytes % W || page_bytes > (1LL << 30))
+        return refuse(PKV_ERR_UNSUPPORTED, call,
+                      W == 16 ? "page_bytes and layer_bytes must be multiples of 16, a page at most 2^30 bytes"
+                              : "bytes of block scales must be multiples of 4, at most 2^30 a page");
+    if (n == 0 || num_layers == 0 || page_bytes == 0)
+        return PKV_OK;
+    if (!k || !v || !src || !dst)
+        return refuse(PKV_ERR_INVALID_ARG, call, "a required pointer is NULL");
+    if (misaligned(k, 16) || misaligned(v, 16) || misaligned(src, 4) || misaligned(dst, 4) || misaligned(count, 4) ||
+        misaligned(status, 4))
+        return refuse(PKV_ERR_INVALID_ARG, call, "caches must be 16-byte aligned, the others 4-byte");
+    p.k = (uint8_t *)k;
+    p.v = (uint8_t *)v;
+    p.layer_bytes = layer_bytes;
+    p.num_layers = num_layers;
+    p.num_pages = num_pages;
+    p.granules = (int32_t)(page_bytes / W);
+    p.n = n;
+    p.src = src;
+    p.dst = dst;
+    p.count = count;
+    p.status = status;
+    return PKV_OK;
+}
+
+bool nothing(const CopyParams &p) { return p.n == 0; }
+
+template <typename Granule>
+cudaError_t launch_copy(const CopyParams &p, void *stream)
+{
+    int dev = 0, sms = 148;
+    if (cudaGetDevice(&dev) == cudaSuccess)
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    const int64_t tiles = ((int64_t)p.n * p.granules + kTile - 1) / kTile * 2 * p.num_layers;
+    const int grid = (int)(tiles < sms * 8LL ? tiles : sms * 8LL);
+    return launch(copy_kernel<Granule>, grid, kCopyThreads, 1, stream, p);
 }
 
 }  // namespace
@@ -883,36 +934,34 @@ PKV_API int pkv_copy_pages(void *k_cache, void *v_cache, int32_t num_layers, int
     using namespace pkv;
     NvtxRange range("pkv_copy_pages");
     set_last_error("");
-    if (n < 0 || num_layers < 0 || num_pages < 0 || page_bytes < 0 || layer_bytes < 0)
-        return refuse(PKV_ERR_INVALID_ARG, "pkv_copy_pages", "negative size");
-    if (page_bytes % 16 || layer_bytes % 16 || page_bytes > (1LL << 30))
-        return refuse(PKV_ERR_UNSUPPORTED, "pkv_copy_pages",
-                      "page_bytes and layer_bytes must be multiples of 16, a page at most 2^30 bytes");
-    if (n == 0 || num_layers == 0 || page_bytes == 0)
-        return PKV_OK;
-    if (!k_cache || !v_cache || !src || !dst)
-        return refuse(PKV_ERR_INVALID_ARG, "pkv_copy_pages", "a required pointer is NULL");
-    if (misaligned(k_cache, 16) || misaligned(v_cache, 16) || misaligned(src, 4) || misaligned(dst, 4) ||
-        misaligned(count, 4) || misaligned(status, 4))
-        return refuse(PKV_ERR_INVALID_ARG, "pkv_copy_pages", "caches must be 16-byte aligned, the others 4-byte");
-    CopyParams p{};
-    p.k = (uint8_t *)k_cache;
-    p.v = (uint8_t *)v_cache;
-    p.layer_bytes = layer_bytes;
-    p.num_layers = num_layers;
-    p.num_pages = num_pages;
-    p.granules = (int32_t)(page_bytes / 16);
-    p.n = n;
-    p.src = src;
-    p.dst = dst;
-    p.count = count;
-    p.status = status;
-    int dev = 0, sms = 148;
-    if (cudaGetDevice(&dev) == cudaSuccess)
-        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    const int64_t tiles = ((int64_t)n * p.granules + kTile - 1) / kTile * 2 * num_layers;
-    const int grid = (int)(tiles < sms * 8LL ? tiles : sms * 8LL);
-    return launched("pkv_copy_pages", launch(copy_kernel, grid, kCopyThreads, 1, stream, p));
+    CopyParams p;
+    const int st = take_copy<uint4>("pkv_copy_pages", k_cache, v_cache, num_layers, layer_bytes, num_pages, page_bytes, src,
+                                    dst, n, count, status, p);
+    return st != PKV_OK || nothing(p) ? st : launched("pkv_copy_pages", launch_copy<uint4>(p, stream));
+}
+
+PKV_API int pkv_copy_pages_blocks(void *k_cache, void *v_cache, void *k_block_scales, void *v_block_scales,
+                                  int32_t num_layers, int64_t layer_bytes, int64_t scale_layer_bytes, int32_t num_pages,
+                                  int64_t page_bytes, int64_t scale_page_bytes, const int32_t *src, const int32_t *dst,
+                                  int32_t n, const int32_t *count, int32_t *status, void *stream)
+{
+    using namespace pkv;
+    const char *call = "pkv_copy_pages_blocks";
+    NvtxRange range(call);
+    set_last_error("");
+    CopyParams p, s;
+    int st = take_copy<uint4>(call, k_cache, v_cache, num_layers, layer_bytes, num_pages, page_bytes, src, dst, n, count,
+                              status, p);
+    const bool whole = scale_page_bytes % 16 == 0 && scale_layer_bytes % 16 == 0;
+    if (st == PKV_OK)
+        st = (whole ? take_copy<uint4> : take_copy<uint32_t>)(call, k_block_scales, v_block_scales, num_layers,
+                                                              scale_layer_bytes, num_pages, scale_page_bytes, src, dst, n,
+                                                              count, status, s);
+    if (st == PKV_OK && !nothing(p))
+        st = launched(call, launch_copy<uint4>(p, stream));
+    if (st == PKV_OK && !nothing(s))
+        st = launched(call, whole ? launch_copy<uint4>(s, stream) : launch_copy<uint32_t>(s, stream));
+    return st;
 }
 
 }  // extern "C"

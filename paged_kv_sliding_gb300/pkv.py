@@ -53,7 +53,7 @@ EXPORTED = ("pkv_plan_create", "pkv_run", "pkv_merge_state", "pkv_plan_destroy",
             "pkv_build_kv_indices", "pkv_plan_create_sinks", "pkv_norm_rope_append",
             "pkv_pages_workspace", "pkv_pages_extend", "pkv_pages_fork", "pkv_pages_free",
             "pkv_pages_compact", "pkv_copy_pages", "pkv_run_blocks", "pkv_norm_rope_append_blocks",
-            "pkv_gather_kv", "pkv_plan_create_shared")
+            "pkv_gather_kv", "pkv_plan_create_shared", "pkv_copy_pages_blocks")
 
 
 class PkvError(RuntimeError):
@@ -239,7 +239,8 @@ def load_library(path: Optional[str] = None):
                            ("pkv_pages_fork", [pool, vp, vp, i32, vp, vp, vp]),
                            ("pkv_pages_free", [pool, vp, i32, vp]),
                            ("pkv_pages_compact", [pool, pool, vp, vp, i32, vp, vp]),
-                           ("pkv_copy_pages", [vp, vp, i32, i64, i32, i64, vp, vp, i32, vp, vp, vp])):
+                           ("pkv_copy_pages", [vp, vp, i32, i64, i32, i64, vp, vp, i32, vp, vp, vp]),
+                           ("pkv_copy_pages_blocks", [vp, vp, vp, vp, i32, i64, i64, i32, i64, i64, vp, vp, i32, vp, vp, vp])):
             getattr(lib, name).argtypes = args
             getattr(lib, name).restype = ctypes.c_int
         lib.pkv_abi_version.argtypes = []
@@ -878,11 +879,13 @@ class PagePool:
 
 
 def copy_pages(k_cache: torch.Tensor, v_cache: torch.Tensor, src: torch.Tensor, dst: torch.Tensor,
-               count: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None, stream=None):
+               count: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None, stream=None,
+               k_block_scales: Optional[torch.Tensor] = None, v_block_scales: Optional[torch.Tensor] = None):
     """Page dst[i] of both caches becomes page src[i]. Caches [num_pages, P, H_kv, d], or
     [layers, num_pages, P, H_kv, d] for every layer at once, contiguous, of any type; src
     and dst int32, negative ids skipped; count: a device int32 of how many pairs are
-    meant (default: all)."""
+    meant (default: all). The block scales of a 4-bit cache ([..., d / 16]) are copied with it when
+    they are given."""
     lib = _lib or load_library()
     shape, dev = k_cache.shape, torch.cuda.current_device()
     if shape != v_cache.shape or k_cache.dtype != v_cache.dtype or len(shape) not in (4, 5):
@@ -904,6 +907,19 @@ def copy_pages(k_cache: torch.Tensor, v_cache: torch.Tensor, src: torch.Tensor, 
     layers = shape[0] if len(shape) == 5 else 1
     pages = shape[-4]
     layer_bytes = k_cache.numel() * k_cache.element_size() // layers if layers else 0
+    if k_block_scales is not None or v_block_scales is not None:
+        if _KV_CODES.get(k_cache.dtype) != PKV_FP4_E2M1:
+            raise ValueError("block scales belong to 4-bit caches")
+        _block_scales(k_cache, k_block_scales, "k_block_scales")
+        _block_scales(v_cache, v_block_scales, "v_block_scales")
+        if k_block_scales.get_device() != dev or v_block_scales.get_device() != dev:
+            raise ValueError("the block scales must be on the current CUDA device")
+        scale_bytes = k_block_scales.numel() // layers if layers else 0
+        _check(lib.pkv_copy_pages_blocks(k_cache.data_ptr(), v_cache.data_ptr(), k_block_scales.data_ptr(),
+                                         v_block_scales.data_ptr(), layers, layer_bytes, scale_bytes, pages,
+                                         layer_bytes // pages if pages else 0, scale_bytes // pages if pages else 0, ptrs[0],
+                                         ptrs[1], src.numel(), ptrs[2], ptrs[3], _stream_handle(stream)), "pkv_copy_pages_blocks")
+        return
     _check(lib.pkv_copy_pages(k_cache.data_ptr(), v_cache.data_ptr(), layers, layer_bytes, pages,
                               layer_bytes // pages if pages else 0, ptrs[0], ptrs[1], src.numel(), ptrs[2], ptrs[3],
                               _stream_handle(stream)), "pkv_copy_pages")

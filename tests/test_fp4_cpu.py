@@ -162,6 +162,26 @@ def test_noalloc_decode_refuses_4_bit_caches(lib):
     assert lib.pkv_decode_noalloc(ctypes.byref(d), None, None, None, None, None, None) == pkv.PKV_ERR_UNSUPPORTED
 
 
+def test_bad_copies_with_block_scales(lib):
+    p, odd = ctypes.c_void_p(0x1000), ctypes.c_void_p(0x1004)
+
+    def call(k=p, v=p, ks=p, vs=p, layers=2, layer_bytes=1 << 20, scale_layer=4000, pages=8, page_bytes=320, scale_page=40,
+             src=p, dst=p, n=2, count=None, status=None):
+        return lib.pkv_copy_pages_blocks(k, v, ks, vs, layers, layer_bytes, scale_layer, pages, page_bytes, scale_page, src, dst,
+                                         n, count, status, None)
+
+    for over in (dict(n=-1), dict(layers=-1), dict(pages=-1), dict(page_bytes=-16), dict(layer_bytes=-16), dict(scale_page=-4),
+                 dict(scale_layer=-4), dict(k=None), dict(v=None), dict(ks=None), dict(vs=None), dict(src=None), dict(dst=None),
+                 dict(k=odd), dict(v=odd), dict(ks=odd), dict(vs=odd), dict(src=ctypes.c_void_p(0x1001)),
+                 dict(count=ctypes.c_void_p(0x1002)), dict(status=ctypes.c_void_p(0x1002))):
+        assert call(**over) == pkv.PKV_ERR_INVALID_ARG, over
+    for over in (dict(page_bytes=40), dict(layer_bytes=1000), dict(page_bytes=1 << 31), dict(scale_page=42),
+                 dict(scale_layer=4002), dict(scale_page=1 << 31)):
+        assert call(**over) == pkv.PKV_ERR_UNSUPPORTED, over
+    for over in (dict(n=0), dict(layers=0)):
+        assert call(**over, k=None, ks=None) == pkv.PKV_OK, over
+
+
 def test_run_without_a_plan(lib):
     assert lib.pkv_run_blocks(*[None] * 9) == pkv.PKV_ERR_INVALID_ARG
 
@@ -235,4 +255,34 @@ def test_a_gather_refuses_what_does_not_fit(fake_lib, over):  # noqa: F811
     over = {k: made[v]() if isinstance(v, str) else v for k, v in over.items()}
     with pytest.raises(ValueError):
         _bind_gather(**over)
+    assert not fake_lib.calls
+
+
+# ---------------------------------------------------------------- copies of pages
+def _bind_copy(dtype=torch.uint8, shape=(3, 6, 5, 2, 32), **over):
+    i = _dev(2, dtype=torch.int32)
+    scales = {x + "_block_scales": _dev(*shape[:-1], shape[-1] // 8, dtype=torch.float8_e4m3fn) for x in "kv"}
+    pkv.copy_pages(_dev(*shape, dtype=dtype), _dev(*shape, dtype=dtype), i, i, **(scales | over))
+
+
+def test_a_copy_takes_block_scales_along(fake_lib):  # noqa: F811
+    _bind_copy()
+    name, args = fake_lib.calls[-1]
+    assert name == "pkv_copy_pages_blocks" and len(args) == 16
+    assert args[4:10] == (3, 6 * 5 * 2 * 32, 6 * 5 * 2 * 4, 6, 5 * 2 * 32, 5 * 2 * 4)
+    _bind_copy(shape=(6, 5, 2, 32))
+    assert fake_lib.calls[-1][1][4:10] == (1, 6 * 5 * 2 * 32, 6 * 5 * 2 * 4, 6, 5 * 2 * 32, 5 * 2 * 4)
+    _bind_copy(k_block_scales=None, v_block_scales=None)
+    assert fake_lib.calls[-1][0] == "pkv_copy_pages"
+
+
+@pytest.mark.parametrize("over", [
+    dict(k_block_scales=None), dict(v_block_scales=None), dict(dtype=torch.float8_e4m3fn),
+    dict(k_block_scales=torch.zeros(3, 6, 5, 2, 4, dtype=torch.float8_e4m3fn)),  # host memory
+    dict(v_block_scales=_dev(3, 6, 5, 2, 2, dtype=torch.float8_e4m3fn)),
+    dict(k_block_scales=_dev(2, 6, 5, 2, 4, dtype=torch.float8_e4m3fn)),
+    dict(k_block_scales=_dev(3, 6, 5, 2, 4, dtype=torch.float32))])
+def test_copies_refuse_wrong_block_scales(fake_lib, over):  # noqa: F811
+    with pytest.raises(ValueError):
+        _bind_copy(**over)
     assert not fake_lib.calls

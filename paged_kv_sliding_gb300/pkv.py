@@ -333,6 +333,8 @@ class Plan:
     Host index arrays are copied by the library.
     """
 
+    _fp4_page = None  # 4-bit caches: the shape of a page
+
     def __init__(self, *, kind: str, kv_indptr, num_qo_heads: int, num_kv_heads: int, head_dim: int,
                  kv_indices: Optional[torch.Tensor] = None, kv_last_page_len=None,
                  page_size: int = 1, num_pages: int = 0, window_left: int = -1, causal: bool = True,
@@ -404,6 +406,8 @@ class Plan:
         d.wait_limit_us = int(wait_limit_us)
         d.wait_probe = 1 if wait_probe else 0
         self._desc = d
+        if d.kv_dtype == PKV_FP4_E2M1:
+            self._fp4_page = (d.page_size, d.num_kv_heads, d.head_dim // 2)
         caps = None
         if capacity is not None:
             caps = PlanCaps()
@@ -471,6 +475,11 @@ class Plan:
                 raise ValueError(f"{name} must be a contiguous CUDA {dt} tensor")
         blocks = self._kv_torch == torch.uint8
         if blocks:
+            # (uint8 may be bytes of another width, of which the scales' shape says nothing)
+            page = self._fp4_page
+            if page is not None and not (k_cache.shape[1:] == v_cache.shape[1:] == page and
+                                         min(k_cache.shape[0], v_cache.shape[0]) >= self._desc.num_pages):
+                raise ValueError(f"k_cache and v_cache must be [{self._desc.num_pages}, {page[0]}, {page[1]}, {page[2]}] bytes")
             _block_scales(k_cache, k_block_scales, "k_block_scales")
             _block_scales(v_cache, v_block_scales, "v_block_scales")
         elif k_block_scales is not None or v_block_scales is not None:

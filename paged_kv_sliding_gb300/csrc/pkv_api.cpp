@@ -690,7 +690,20 @@ int validate_groups(const pkv_plan_desc &d, const std::vector<HostRequest> &reqs
     return PKV_OK;
 }
 
-// Fewest prefix keys that a group's requests see together for which the prefix is computed apart.
+// Fewest prefix keys that a group's requests see together for which the prefix is computed apart: a
+// floor for what is a few tiles at most, and no comparison with the ordinary plan, which is faster for
+// short prefixes and for few requests over narrow caches. Measured, ordinary / shared in us, 8 KV
+// heads of 128, 32 query heads, 100 keys of each request's own:
+//                                 80 keys      256          1024         4096
+//     1 group of 4, bf16          6.1 / 12.2   7.1 / 8.8    10.2 / 9.1   14.4 / 10.9
+//     1 group of 16, bf16         6.3 / 12.8   7.5 / 9.2    16.4 / 9.7   33.4 / 17.2
+//     1 group of 4, E4M3          5.6 / 12.6   6.3 / 10.0   10.5 / 10.1  13.8 / 12.0
+//     1 group of 4, 4 bits        4.9 / 12.8   6.0 / 10.6   8.4 / 10.7   11.8 / 12.5
+//     8 groups of 2, bf16         6.3 / 12.5   7.5 / 9.1    18.6 / 17.8  34.5 / 32.1
+//     8 groups of 8, bf16         9.2 / 16.4   14.7 / 18.7  38.6 / 23.4  114 / 38.5
+//     8 groups of 2, 4 bits       4.9 / 12.7   6.1 / 10.9   11.2 / 15.8  22.9 / 40.2
+//     8 groups of 8, 4 bits       7.6 / 14.0   11.3 / 11.7  24.1 / 20.8  69.9 / 40.3
+// The caller says which groups are shared (pkv.h has the rule of thumb).
 constexpr int64_t kMinSharedKeys = 64;
 // Fewest tiles of an item list: below, fewer CTAs share the work.
 constexpr int64_t kMinSharedTiles = 2;
@@ -700,9 +713,14 @@ constexpr int64_t kMinSharedTiles = 2;
 // 7 + 7 k + c n, with c = 0.96 for a tile of 64 KB (K and V) by TMA and 1.4 where rows are
 // copied or widened; the decode kernel its bytes at 6.8 TB/s, plus the SMs' share that the
 // prefix has. The prefix is to end in 0.85 of the whole time, as its states are merged last.
-// Measured, with 152 and the choice, in us: 128 requests behind 8192 keys, 8 KV heads of 128, bf16
-// 90 / 73; 6 groups of up to 48 behind up to 6000, bf16 107 / 97, E4M3 117 / 111 (widened tiles
-// then took 2 us; 1.2 to 1.92 are within 2.5% of each other).
+// Measured, with as many CTAs as there are SMs and the choice, in us: 128 requests behind 8192 keys,
+// 8 KV heads of 128, bf16 87.6 / 72.0, in pages of 5 118 / 111, E4M3 80.2 / 74.9, 4 bits 62.2 / 61.1;
+// 6 groups of up to 48 behind up to 6000, bf16 104.6 / 95.4, E4M3 96.6 / 92.6, 4 bits 78.0 / 78.4; 128
+// behind 4096, 4 heads of 256, bf16 82.5 / 64.0, E4M3 73.3 / 64.4, 4 bits 54.4 / 44.7. The one 1.4
+// stands for tiles of 1.2 us (rows copied), 1.6 (8 bits) and 1.8 (4 bits): with these in its
+// place every one of 31 batches was within 1%. Nor does it matter that the 4-bit decode keeps to 0.75 of
+// the 6.8 TB/s, and that states are not counted: one KV head with 16 requests behind 60000 keys,
+// in 150 pieces, takes 31.1 us, an ordinary plan 59.0.
 int64_t choose_prefix_ctas(const pkv_plan_desc &d, const std::vector<int64_t> &units, int64_t total, int64_t own_keys,
                            int n_sm)
 {
@@ -917,7 +935,10 @@ void build_shared_schedule(const pkv_plan_desc &d, const std::vector<HostRequest
                                           sc.reqs[b].kv_len, sc.reqs[b].kv_page_begin, 0, prefix_pieces});
                 }
     }
-    // CTAs that wait for the prefix keep others out where not all of them fit beside it.
+    // CTAs that wait for the prefix keep others out where not all of them fit beside it: two to an SM
+    // taken for every kernel, of which one (head_dim 256, bf16) to four fit. Measured, with 1, 2 and 4 in
+    // its place: heads of 256, 24 requests behind 4096 keys 27.1 / 26.2 / 26.1 us, 64 37.5 / 37.5 / 39.6,
+    // 128 64.0 / 64.0 / 84.5; 28 more batches of every type within 4% of each other.
     if ((int64_t)sc.d_items.size() > 2 * (n_sm - n_cta))
         sc.s_merges = std::move(merges);
     auto keys = [](const DecodeItem &it) { return it.j1 - it.j0; };

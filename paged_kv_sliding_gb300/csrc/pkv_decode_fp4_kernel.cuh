@@ -225,7 +225,7 @@ __global__ void __launch_bounds__(Traits<D, HP, NWH>::kThreads, Traits<D, HP, NW
         fence_proxy_async_smem();
     }
     __syncthreads();
-    if (!SHARED)
+    if (!SHARED)  // (see Shared prefixes in pkv_decode_kernel.cuh)
         grid_dependency_wait();
 
     if (warp == NW) {

@@ -45,6 +45,11 @@
 // before the group's last CTA merges them with its own. That is for grids that are on the GPU all
 // at once (p.merge_counters set); in longer ones the waiting CTAs would keep the others out, so
 // they leave a partial state and end, and a launch behind merges (pkv_shared.cu).
+// An assumption about the GPU is in that: q, the page table and the caches are visible to this grid
+// because the prefix's CTAs have waited for the kernel that wrote them before they let this grid start,
+// so that it had ended, and its writes reached L2, before any CTA here began with an empty L1. The
+// programming model promises that to a grid that waits itself; a wait here would last until the prefix
+// has ended, which is what the launch beside it avoids.
 //
 // All waits are bounded (the plan's wait bound, 2 s by default); on expiry
 // PKV_ERR_TIMEOUT is recorded and the CTA winds down after its outstanding copies
@@ -213,7 +218,7 @@ __global__ void __launch_bounds__(DecTraits<D, TT, KV, TPW>::kThreads, DecTraits
     __syncthreads();
     // Everything above reads only the plan's own data; q, the caches and the page
     // table may come from the previous kernel in the stream.
-    if (!SHARED)
+    if (!SHARED)  // (Shared prefixes, above)
         grid_dependency_wait();
 
     if (warp == Tr::kCompute) {

@@ -280,9 +280,11 @@ extern "C" PKV_API int pkv_gather_kv(const pkv_gather_desc *desc, const void *k_
     if (d.total == 0 || d.batch_size == 0)
         return PKV_OK;
     const bool blocks = d.kv_dtype == PKV_FP4_E2M1;
-    if (!k_cache || !v_cache || !kv_indptr || !kv_indices || !out_indptr || !k_out || !v_out)
+    // (arrays of no pages or entries may be NULL: every row is then one that the pages do not hold)
+    if ((d.num_pages > 0 && (!k_cache || !v_cache)) || !kv_indptr || (d.num_indices > 0 && !kv_indices) || !out_indptr ||
+        !k_out || !v_out)
         return refuse(PKV_ERR_INVALID_ARG, "caches, kv_indptr, kv_indices, out_indptr, k_out and v_out are required");
-    if (blocks ? !k_block_scales || !v_block_scales : k_block_scales || v_block_scales)
+    if (blocks ? d.num_pages > 0 && (!k_block_scales || !v_block_scales) : k_block_scales || v_block_scales)
         return refuse(PKV_ERR_INVALID_ARG, "block scales come with 4-bit caches, and these with them");
     for (const void *p : {k_cache, v_cache, k_block_scales, v_block_scales, (const void *)k_out, (const void *)v_out})
         if (misaligned(p, 16))

@@ -118,6 +118,16 @@ def test_gather_missing_or_misaligned_tensors(lib, name):
     assert _gather(lib, pointers={name: 0x1002}) == pkv.PKV_ERR_INVALID_ARG
 
 
+def test_gather_from_no_pages_is_not_refused(lib):
+    """(Without a GPU what passes the checks fails at the launch.)"""
+    empty = ("k_cache", "v_cache", "k_block_scales", "v_block_scales", "kv_indices")
+    if not torch.cuda.is_available():
+        assert _gather(lib, null=empty, num_pages=0, num_indices=0) == pkv.PKV_ERR_CUDA
+        assert _gather(lib, null=("kv_indices",), num_indices=0) == pkv.PKV_ERR_CUDA
+    for name in empty:
+        assert _gather(lib, null=(name,)) == pkv.PKV_ERR_INVALID_ARG
+
+
 def test_gather_of_nothing(lib):
     assert _gather(lib, desc=False) == pkv.PKV_ERR_INVALID_ARG
     assert _gather(lib, total=0) == pkv.PKV_OK and _gather(lib, batch_size=0) == pkv.PKV_OK

@@ -28,8 +28,8 @@
 // SMs, 2.1 us), HPG = 4 otherwise. Measured on 16384 tokens x 48 heads of 128, bf16: 64.5 us
 // = 6.37 TB/s, 0.94 of the copy rate; 8191 tokens of 8 + 2 x 4 heads of 256 into E4M3 22.5 us
 // (with products by one rounded reciprocal 22.15; eight heads to a group, measured with
-// those, 62 and 23.4 us: on the second they stay half empty). Into 4-bit caches the first takes 74.5 us
-// for 354 MB (4.75 TB/s, 0.70 of the copy rate) and the second 26.0: the blocks' shuffles, codes and
+// those, 62 and 23.4 us: on the second they stay half empty). Into 4-bit caches the first takes 74.7 us
+// for 354 MB (4.74 TB/s, 0.70 of the copy rate) and the second 26.1: the blocks' shuffles, codes and
 // quotients are a third of the instructions, and registers keep warps out. With the registers of 9
 // blocks an SM (kFp4Blocks) 74.5 us, of 8 76.2, of 10 79.1, as the compiler likes (7) 80.3. The
 // sums of `square_sum` and k's unfused rotation are 3.4 us of it (71.1 and 25.3 without).
